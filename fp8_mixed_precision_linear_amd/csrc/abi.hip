@@ -247,8 +247,9 @@ fp8_status fp8_cast_rowwise(const void* x_bf16, int64_t rows, int64_t cols, fp8_
                                       scale_inv, y_t, scale_inv_t, stream));
 }
 
-fp8_status fp8_scaled_gemm(const fp8_gemm_args* a, hipStream_t stream) {
-  if (a == nullptr) return FP8_ERR_NULL;
+}  // extern "C"
+
+fp8_status fp8lin::gemm_params(const fp8_gemm_args* a, GemmParams& p) {
   if (a->M < 0 || a->N < 0 || a->K < 0) return FP8_ERR_SHAPE;
   if (!fmt_ok(a->a_fmt) || !fmt_ok(a->b_fmt)) return FP8_ERR_ARG;
   if (!scaling_ok(a->a_scaling) || !scaling_ok(a->b_scaling)) return FP8_ERR_ARG;
@@ -285,7 +286,6 @@ fp8_status fp8_scaled_gemm(const fp8_gemm_args* a, hipStream_t stream) {
     }
   }
   if (a->d_amax && !aligned4(a->d_amax)) return FP8_ERR_ALIGN;
-  GemmParams p;
   p.M = a->M; p.N = a->N; p.K = a->K;
   p.lda = a->lda; p.ldb = a->ldb; p.ldd = a->ldd;
   p.A = a->A; p.a_fmt = a->a_fmt; p.a_scaling = a->a_scaling; p.a_sinv = a->a_scale_inv;
@@ -296,8 +296,18 @@ fp8_status fp8_scaled_gemm(const fp8_gemm_args* a, hipStream_t stream) {
   p.d_scale = fp8_out ? a->d_scale : nullptr;
   p.D_t = fp8_out ? a->D_t : nullptr;
   p.ldt = a->ldt;
+  return FP8_OK;
+}
+
+extern "C" {
+
+fp8_status fp8_scaled_gemm(const fp8_gemm_args* a, hipStream_t stream) {
+  if (a == nullptr) return FP8_ERR_NULL;
+  GemmParams p;
+  const fp8_status st = gemm_params(a, p);
+  if (st != FP8_OK) return st;
   // the quantising epilogue lives in the large-tile kernel only
-  if (fp8_out && p.K > 0 && p.M > 0 && p.N > 0 && !gemm_big_supported(p)) return FP8_ERR_UNSUPPORTED;
+  if (p.d_fp8 && p.K > 0 && p.M > 0 && p.N > 0 && !gemm_big_supported(p)) return FP8_ERR_UNSUPPORTED;
   return launched(launch_gemm(p, stream));
 }
 

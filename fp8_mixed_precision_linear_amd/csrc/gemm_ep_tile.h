@@ -1,0 +1,188 @@
+// gemm_ep_tile.h -- the FP8 product with the linear's epilogue on tiles of
+// BM x BN, for outputs that the 256 x 256 tiles of the large kernels would not
+// spread over the card; instantiated by gemm_ep_tile.hip.
+//
+// A workgroup of four wavefronts takes one tile and, where tiles alone would
+// leave compute units idle, one of `splits` parts of K; the parts' binary32
+// sums go to the workspace and k_ep_join adds them in order and applies the
+// epilogue.  Operands come through LDS in steps of 128 bytes of K, STAGES
+// stages deep, by buffer loads straight into LDS (layout, swizzle and
+// fragments as in gemm_big_kernel.h); rows past an operand's end fail the
+// buffer's range check and read zeros, and so do chunks past K.
+// Per-tensor and per-row scales are applied to the whole sum; with block scales
+// (BLOCK) every step's product is promoted into the binary32 accumulator by the
+// step's row and column scales, which arrive in LDS with the operands.
+#pragma once
+
+#include "gemm_big_kernel.h"
+#include "gemm_ep.h"
+
+namespace fp8lin {
+
+namespace {
+
+constexpr int EP_THREADS = 256;
+
+// One step's scale of an operand's row: the inverse scales' base and the row's
+// offset in it.
+__device__ __forceinline__ int64_t scale_base(int scaling, int64_t rows, int64_t kb) {
+  return scaling == 0 ? 0 : (scaling == 1 ? kb * rows : kb * ((rows + 127) / 128));
+}
+__device__ __forceinline__ int64_t scale_row(int scaling, int64_t row) {
+  return scaling == 0 ? 0 : (scaling == 1 ? row : row / 128);
+}
+
+// WM x WN wavefronts of (16 TI) x (16 TJ).
+template <int AF, int BF, bool BLOCK, bool OUT8, int WM, int WN, int TI, int TJ, int STAGES>
+__global__ void __launch_bounds__(EP_THREADS) k_ep_tile(GemmParams p, EpParams e, int tiles_m, int tiles_n) {
+  constexpr int BM_ = 16 * TI * WM, BN_ = 16 * TJ * WN;
+  static_assert(WM * WN == 4 && BM_ % 32 == 0 && BN_ % 32 == 0, "four wavefronts");
+  constexpr int ABYTES = BM_ * BK, BBYTES = BN_ * BK;
+  constexpr int SCALES = BLOCK ? 4 * ((BM_ + 63) / 64 * 64 + (BN_ + 63) / 64 * 64) : 0;
+  constexpr int SA0 = ABYTES + BBYTES, SB0 = SA0 + (BM_ + 63) / 64 * 64 * 4;
+  constexpr int STAGE_ = ABYTES + BBYTES + SCALES;
+  constexpr int WREG = 64 * 16 * TJ + (OUT8 ? 16 * TJ * (16 * TI + 16) : 0);   // epilogue bytes per wavefront
+  constexpr int LDS_ = STAGES * STAGE_ > 4 * WREG ? STAGES * STAGE_ : 4 * WREG;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_];
+  __shared__ float rs_tab[BLOCK ? 1 : BM_ + BN_];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int g = lane >> 4, l16 = lane & 15;
+  const int64_t M = p.M, N = p.N, K = p.K;
+
+  // tile id as in the large kernels: contiguous runs per XCD, 8 tile-rows at a time
+  const int nblk = tiles_m * tiles_n;
+  int bid = blockIdx.x;
+  if ((nblk & 7) == 0) bid = (bid & 7) * (nblk >> 3) + (bid >> 3);
+  const int group = bid / (GROUP_M * tiles_n), first_m = group * GROUP_M;
+  const int gm = min(tiles_m - first_m, GROUP_M), in_group = bid - group * GROUP_M * tiles_n;
+  const int tm = first_m + in_group % gm, tn = in_group / gm;
+  const int64_t m0 = (int64_t)tm * BM_, n0 = (int64_t)tn * BN_;
+  const int64_t rows_a = min((int64_t)BM_, M - m0), rows_b = min((int64_t)BN_, N - n0);
+  const i32x4 ra = make_rsrc(p.A + m0 * p.lda, (uint32_t)(rows_a * p.lda));
+  const i32x4 rb = make_rsrc(p.B + n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
+  const int lda = (int)p.lda, ldb = (int)p.ldb;
+
+  // this workgroup's part of the K steps
+  const int nk_all = (int)((K + BK - 1) / BK);
+  const int z = blockIdx.y;
+  const int kb0 = (int)((int64_t)nk_all * z / e.splits), kb1 = (int)((int64_t)nk_all * (z + 1) / e.splits);
+
+  // a wavefront's share of a stage: 8 rows per instruction
+  constexpr int QA = BM_ / 32, QB = BN_ / 32;
+  auto load = [&](int kb, int stage) {
+    const uint32_t base = lds_addr(lds) + stage * STAGE_;
+#pragma unroll
+    for (int it = 0; it < QA + QB; ++it) {
+      const bool a = it < QA;
+      const int row = (a ? (BM_ / 4) * wave + 8 * it : (BN_ / 4) * wave + 8 * (it - QA)) + (lane >> 3);
+      const int kc = kb * BK + 16 * ((lane & 7) ^ swz(row));
+      const uint32_t dst =
+          base + (a ? 0 : ABYTES) + ((a ? (BM_ / 4) * wave + 8 * it : (BN_ / 4) * wave + 8 * (it - QA))) * BK;
+      dma16(dst, kc < (int)K ? (uint32_t)(row * (a ? lda : ldb)) + (uint32_t)kc : kOOB, a ? ra : rb);
+    }
+    if constexpr (BLOCK) {   // chunks of 64 row scales, A's then B's
+      constexpr int CA = (BM_ + 63) / 64, CB = (BN_ + 63) / 64, PER = (CA + CB + 3) / 4;
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int ch = min(wave * PER + u, CA + CB - 1);   // the last chunk may be fetched twice
+        const bool a = ch < CA;
+        const int64_t rows = a ? M : N, r0 = a ? m0 : n0;
+        const int sc = a ? p.a_scaling : p.b_scaling;
+        const int r = 64 * (a ? ch : ch - CA) + lane;
+        const int64_t first = scale_row(sc, r0);
+        const int64_t last = scale_row(sc, rows - 1);
+        const float* s = (a ? p.a_sinv : p.b_sinv) + scale_base(sc, rows, kb) + first;
+        const i32x4 rs = make_rsrc(s, (uint32_t)min((int64_t)4 * (last - first + 1), (int64_t)4 * BK * 4));
+        const uint32_t off = (uint32_t)(4 * (min(scale_row(sc, r0 + r), last) - first));
+        dma4(base + (a ? SA0 : SB0) + 256 * (a ? ch : ch - CA), off, rs);
+      }
+    }
+  };
+
+  v4f acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  if constexpr (!BLOCK) {
+    for (int r = tid; r < BM_ + BN_; r += EP_THREADS) {
+      const bool a = r < BM_;
+      const int64_t row = min((a ? m0 + r : n0 + r - BM_), (a ? M : N) - 1);
+      const bool per_row = (a ? p.a_scaling : p.b_scaling) == 5;
+      rs_tab[r] = K > 0 ? (a ? p.a_sinv : p.b_sinv)[per_row ? row : 0] : 0.0f;
+    }
+  }
+
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s)
+    if (kb0 + s < kb1) load(kb0 + s, s);
+  for (int kb = kb0; kb < kb1; ++kb) {
+    const int st = (kb - kb0) % STAGES;
+    // Every wavefront's share of this step's stage has to be in LDS, and every
+    // wavefront done with the stage that the next load fills.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (kb + STAGES - 1 < kb1) load(kb + STAGES - 1, (st + STAGES - 1) % STAGES);
+    const uint8_t* S = lds + st * STAGE_;
+    v8i b[TJ];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) b[j] = frag(S + ABYTES, wn * 16 * TJ + 16 * j + l16, g);
+    float4 sb[BLOCK ? TJ : 1];
+    if constexpr (BLOCK) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        sb[j] = *reinterpret_cast<const float4*>(S + SB0 + 4 * (wn * 16 * TJ + 16 * j + 4 * g));
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int row = wm * 16 * TI + 16 * i + l16;
+      const v8i a = frag(S, row, g);
+      float sa = 1.0f;
+      if constexpr (BLOCK) sa = *reinterpret_cast<const float*>(S + SA0 + 4 * row);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        if constexpr (BLOCK) {
+          const v4f part = mfma<BF, AF>(b[j], a, v4f{0.f, 0.f, 0.f, 0.f});
+          acc[i][j][0] = __builtin_fmaf(part[0] * sa, sb[j].x, acc[i][j][0]);
+          acc[i][j][1] = __builtin_fmaf(part[1] * sa, sb[j].y, acc[i][j][1]);
+          acc[i][j][2] = __builtin_fmaf(part[2] * sa, sb[j].z, acc[i][j][2]);
+          acc[i][j][3] = __builtin_fmaf(part[3] * sa, sb[j].w, acc[i][j][3]);
+        } else {
+          acc[i][j] = mfma<BF, AF>(b[j], a, acc[i][j]);
+        }
+      }
+    }
+  }
+  __syncthreads();   // the stages are free for the epilogue, rs_tab is written
+
+  auto deq = [&](int i, int j, int q, float x) -> float {
+    if constexpr (BLOCK) return x;
+    else
+      return (x * rs_tab[wm * 16 * TI + 16 * i + l16]) * rs_tab[BM_ + wn * 16 * TJ + 16 * j + 4 * g + q];
+  };
+  const int64_t r0 = m0 + wm * 16 * TI, c0 = n0 + wn * 16 * TJ;
+  uint8_t* wl = lds + wave * WREG;
+  if (e.splits > 1) {   // this part's sums, [split][M][ldw]
+    EpParams es = {};
+    es.splits = 1;
+    GemmParams ps = p;
+    ps.D = e.sums + (int64_t)z * M * e.ldw;
+    ps.ldd = e.ldw;
+    ps.d_f32 = 1;
+    ps.d_amax = nullptr;
+    EpWave<16 * TJ, false> w(ps, es, c0, lane);
+    w.template tile<TI, TJ>(acc, deq, r0, c0, wl);
+    return;
+  }
+  EpWave<16 * TJ, OUT8> w(p, e, c0, lane);
+  w.template tile<TI, TJ>(acc, deq, r0, c0, wl);
+  w.put_dbias((int64_t)tm * WM + wm);
+  if (p.d_amax) ep_amax<4>(p.d_amax, w.amax_bits(), lane, wave);
+}
+
+}  // namespace
+
+}  // namespace fp8lin

@@ -1,0 +1,140 @@
+// gemm_ep_tile.hip -- the FP8 product with the linear's epilogue: its tile
+// kernels, the join of K parts, the bias gradient's join and the dispatch.
+#include "gemm_ep_tile.h"
+
+namespace fp8lin {
+
+namespace {
+
+// The parts' sums added in order, then the epilogue: a wavefront takes 16 rows
+// of 128 columns, a workgroup 64 rows.
+template <bool OUT8>
+__global__ void __launch_bounds__(256) k_ep_join(GemmParams p, EpParams e) {
+  constexpr int TS = 32;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[OUT8 ? 4 * 128 * TS : 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n0 = (int64_t)blockIdx.x * 128, m0 = (int64_t)blockIdx.y * 64 + 16 * wave;
+  EpWave<128, OUT8> w(p, e, n0, lane);
+  constexpr int RPL = EpWave<128, OUT8>::RPL;
+  float v[RPL][8], o[RPL][8];
+  w.fetch(m0, o);
+#pragma unroll
+  for (int t = 0; t < RPL; ++t) {
+    const int64_t m = m0 + w.rg * RPL + t;
+    const int n = m < p.M ? w.nv : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[t][k] = 0.0f;
+    for (int z = 0; z < e.splits; ++z) {
+      float s[8];
+      load8(e.sums, 1, ((int64_t)z * p.M + m) * e.ldw + w.c, n, s);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[t][k] += s[k];
+    }
+  }
+  uint8_t* tl = lds + (OUT8 ? wave * 128 * TS : 0);
+  w.template strip<TS>(m0, v, o, tl, 0);
+  if constexpr (OUT8) {
+    asm volatile("" ::: "memory");
+    if (p.D_t) w.template flush_t<TS, 16>(tl, m0, n0);
+  }
+  w.put_dbias((int64_t)blockIdx.y * 4 + wave);
+  if (p.d_amax) ep_amax<4>(p.d_amax, w.amax_bits(), lane, wave);
+}
+
+// dbias[n] = sum of the parts' column sums, 64 columns by 16 parts at a time,
+// in a fixed order.
+__global__ void __launch_bounds__(1024) k_ep_dbias(const float* part, int64_t parts, int64_t N, void* dbias, int f32) {
+  __shared__ float lds[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (n < N)
+    for (int64_t q = wave; q < parts; q += 16) s += part[q * N + n];
+  lds[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || n >= N) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += lds[w][lane];
+  if (f32) reinterpret_cast<float*>(dbias)[n] = s;
+  else reinterpret_cast<uint16_t*>(dbias)[n] = f32_to_bf16_rne(s);
+}
+
+template <int AF, int BF, bool BLOCK, bool OUT8>
+hipError_t launch_tile(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s) {
+  const int tiles_m = (int)((p.M + plan.bm - 1) / plan.bm), tiles_n = (int)((p.N + plan.bn - 1) / plan.bn);
+  const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)plan.splits), block(EP_THREADS);
+  hipLaunchKernelGGL((k_ep_tile<AF, BF, BLOCK, OUT8, 2, 2, 4, 4, 2>), grid, block, 0, s, p, e, tiles_m, tiles_n);
+  return hipGetLastError();
+}
+
+template <bool BLOCK, bool OUT8>
+hipError_t launch_fmt(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s) {
+  if (p.a_fmt == 0 && p.b_fmt == 0) return launch_tile<0, 0, BLOCK, OUT8>(p, e, plan, s);
+  if (p.a_fmt == 1 && p.b_fmt == 0) return launch_tile<1, 0, BLOCK, OUT8>(p, e, plan, s);
+  if (p.a_fmt == 0 && p.b_fmt == 1) return launch_tile<0, 1, BLOCK, OUT8>(p, e, plan, s);
+  return launch_tile<1, 1, BLOCK, OUT8>(p, e, plan, s);
+}
+
+}  // namespace
+
+EpPlan ep_plan(const GemmParams& p) {
+  EpPlan plan = {};
+  plan.bm = 128;
+  plan.bn = 128;
+  plan.splits = 1;
+  plan.parts = (p.M + 127) / 128 * 2;   // wavefront rows of the tiles
+  const int64_t tiles = ((p.M + 127) / 128) * ((p.N + 127) / 128), cu = device_cu_count();
+  const int64_t nk = (p.K + BK - 1) / BK;
+  // Split K while the tiles leave compute units without work and every part
+  // keeps at least four steps.
+  int64_t splits = 1;
+  while (splits < 16 && tiles * splits * 2 <= cu && nk / (splits * 2) >= 4) splits *= 2;
+  if (splits > 1) {
+    plan.splits = (int)splits;
+    plan.parts = (p.M + 63) / 64 * 4;   // wavefronts of the join
+  }
+  plan.ldw = (p.N + 7) / 8 * 8;
+  plan.part_bytes = (plan.parts * p.N * 4 + 255) / 256 * 256;
+  plan.sums_bytes = plan.splits > 1 ? plan.splits * p.M * plan.ldw * 4 : 0;
+  return plan;
+}
+
+hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStream_t s) {
+  GemmParams p = p0;
+  // power-of-two block scales are binary32 scales of the same layouts here
+  if (p.a_scaling == 3 || p.a_scaling == 4) p.a_scaling -= 2;
+  if (p.b_scaling == 3 || p.b_scaling == 4) p.b_scaling -= 2;
+  if (p.d_amax && !p.amax_acc) {
+    const hipError_t err = launch_fill_u32(reinterpret_cast<uint32_t*>(p.d_amax), 1, 0u, s);
+    if (err != hipSuccess) return err;
+  }
+  if (p.N == 0) return hipSuccess;
+  const EpPlan plan = ep_plan(p);
+  e.part = reinterpret_cast<float*>(ws);
+  e.sums = reinterpret_cast<float*>(ws + plan.part_bytes);
+  e.ldw = plan.ldw;
+  e.splits = plan.splits;
+  const bool block = !((p.a_scaling == 0 || p.a_scaling == 5) && (p.b_scaling == 0 || p.b_scaling == 5));
+  if (p.M > 0) {
+    hipError_t err;
+    if (block) err = p.d_fp8 ? launch_fmt<true, true>(p, e, plan, s) : launch_fmt<true, false>(p, e, plan, s);
+    else err = p.d_fp8 ? launch_fmt<false, true>(p, e, plan, s) : launch_fmt<false, false>(p, e, plan, s);
+    if (err != hipSuccess) return err;
+    if (plan.splits > 1) {
+      const dim3 grid((unsigned)((p.N + 127) / 128), (unsigned)((p.M + 63) / 64));
+      if (p.d_fp8) hipLaunchKernelGGL((k_ep_join<true>), grid, dim3(256), 0, s, p, e);
+      else hipLaunchKernelGGL((k_ep_join<false>), grid, dim3(256), 0, s, p, e);
+      err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
+  }
+  if (e.dbias) {
+    hipLaunchKernelGGL(k_ep_dbias, dim3((unsigned)((p.N + 63) / 64)), dim3(1024), 0, s, e.part, plan.parts, p.N,
+                       e.dbias, e.bias_f32);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace fp8lin

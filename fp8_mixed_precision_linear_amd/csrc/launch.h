@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/fp8lin.h"
+
 namespace fp8lin {
 
 // Compute units of the current device (queried once per device).
@@ -77,6 +79,9 @@ struct GemmParams {
   int64_t ldt;
 };
 
+// Checks a GEMM's arguments (abi.hip) and, if they are right, fills p.
+fp8_status gemm_params(const fp8_gemm_args* a, GemmParams& p);
+
 hipError_t launch_gemm(const GemmParams& p, hipStream_t s);
 
 // Large-tile GEMM (gemm_big.hip): used when supported (32-bit buffer offsets
@@ -93,5 +98,109 @@ hipError_t launch_gemm_w4_fp8out(const GemmParams& p, hipStream_t s);   // p.d_f
 // (gemm_w4_mx.hip, gemm_w4_mx_fp8out.hip).
 hipError_t launch_gemm_w4_mx(const GemmParams& p, hipStream_t s);
 hipError_t launch_gemm_w4_mx_fp8out(const GemmParams& p, hipStream_t s);   // p.d_fp8 != 0
+
+// ---- operators around the linears (arguments validated by abi_block.hip)
+
+// Norms before and after a block with its gate and residual scale
+// (norm_kernels.hip).  x_f32: type of x and h; p_f32: of the weights, biases
+// and a channel gate; gate_kind: 0 none, 1 per channel, 2 per token (FP32),
+// 3 per element (BF16); gate_act: 0 none, 1 sigmoid, 2 tanh; layer: layer
+// norm, else RMS norm; y8_scaling: 0 per tensor, 5 per row, 1 per 128 columns.
+struct NormParams {
+  int64_t rows, cols;
+  const void* x;
+  int64_t ldx;
+  int x_f32, p_f32, layer, gate_kind, gate_act;
+  const void* z;
+  int64_t ldz;
+  const void *w_post, *b_post, *w_pre, *b_pre, *gate;
+  int64_t ldg;
+  float res_scale, branch_scale, eps;
+  void* h;
+  int64_t ldh;
+  float *stats_z, *stats_h;
+  void* y;
+  int64_t ldy;
+  uint8_t* y8;
+  int64_t ldy8;
+  int y8_fmt, y8_scaling;
+  const float* y8_scale;
+  float *y8_sinv, *y8_amax;
+};
+struct NormGradParams {
+  int64_t rows, cols;
+  const void* dy;
+  int64_t lddy;
+  const void* dh;
+  int64_t lddh;
+  const void* h;
+  int64_t ldh;
+  const float* stats_h;
+  const void* z;
+  int64_t ldz;
+  const float* stats_z;
+  int x_f32, p_f32, layer, gate_kind, gate_act;
+  const void *w_post, *b_post, *w_pre, *gate;
+  int64_t ldg;
+  float res_scale, branch_scale;
+  void* dx;
+  int64_t lddx;
+  void* dz;
+  int64_t lddz;
+  void *dgate;
+  int64_t lddg;
+  void *dw_pre, *db_pre, *dw_post, *db_post;
+  float* part;   // workspace: 4 * norm_parts(rows) * cols floats
+};
+int64_t norm_max_cols();
+int64_t norm_parts(int64_t rows);
+hipError_t launch_norm_fwd(const NormParams& p, hipStream_t s);
+hipError_t launch_norm_bwd(const NormGradParams& p, hipStream_t s);
+
+// Rotary positions (rope_kernels.hip): strides in elements, of tokens (st) and
+// heads (sh).
+struct RopeParams {
+  int64_t tokens, q_heads, k_heads, dim, pairs;
+  const double* freqs;
+  const void* pos;   // NULL: offset + token
+  int64_t offset;
+  int pos_i64, f32, interleaved, inverse, copy_rest;
+  float scale;
+  const void* q;
+  int64_t q_st, q_sh;
+  const void* k;
+  int64_t k_st, k_sh;
+  void* q_out;
+  int64_t qo_st, qo_sh;
+  void* k_out;
+  int64_t ko_st, ko_sh;
+  int tokens_wg, heads_wg;   // set by the launcher
+};
+int64_t rope_max_pairs();
+hipError_t launch_rope(RopeParams p, hipStream_t s);
+hipError_t launch_rope_freqs(double* f, int64_t pairs, double base, int scaling, double factor, double trained,
+                             double low, double high, hipStream_t s);
+
+// The FP8 product with the linear's epilogue (gemm_ep*.hip).
+struct EpParams {
+  int backward, act, bias_f32, res_f32, splits;
+  const void* bias;      // forward
+  const void* residual;  // forward
+  int64_t ldres;
+  float res_scale;
+  const void* aux;       // forward: written (bf16(u)) or NULL; backward: read
+  int64_t ldaux;
+  void* dbias;           // backward; type bias_f32
+  float* part;           // workspace: column sums
+  float* sums;           // workspace: [splits][M][ldw]
+  int64_t ldw;
+};
+// How a product is cut: tile, parts of K, rows of column sums, workspace.
+struct EpPlan {
+  int bm, bn, splits;
+  int64_t parts, ldw, part_bytes, sums_bytes;
+};
+EpPlan ep_plan(const GemmParams& p);
+hipError_t launch_gemm_ep(const GemmParams& p, EpParams e, uint8_t* ws, hipStream_t s);
 
 }  // namespace fp8lin

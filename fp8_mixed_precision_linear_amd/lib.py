@@ -23,6 +23,13 @@ SCALE_1x128_POW2, SCALE_128x128_POW2 = 3, 4
 SCALE_ROW = 5
 OUT_BF16, OUT_F32, OUT_E4M3, OUT_E5M2 = 0, 1, 2, 3
 AMAX_MAX, AMAX_MOST_RECENT = 0, 1
+DT_BF16, DT_F32 = 0, 1
+NORM_RMS, NORM_LAYER = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+GATE_LINEAR, GATE_SIGMOID, GATE_TANH = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = 0, 1, 2, 3
 
 STATUS = {0: "FP8_OK", 1: "FP8_ERR_NULL", 2: "FP8_ERR_SHAPE", 3: "FP8_ERR_ALIGN",
           4: "FP8_ERR_UNSUPPORTED", 5: "FP8_ERR_LAUNCH", 6: "FP8_ERR_ARG"}
@@ -45,6 +52,54 @@ class GemmArgs(C.Structure):
                 ("accumulate", C.c_int),
                 ("d_scale", C.c_void_p), ("D_t", C.c_void_p), ("ldt", C.c_int64),
                 ("amax_accumulate", C.c_int)]
+
+
+class NormArgs(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64),
+                ("kind", C.c_int), ("stream_dtype", C.c_int), ("param_dtype", C.c_int),
+                ("eps", C.c_float), ("res_scale", C.c_float), ("branch_scale", C.c_float),
+                ("x", C.c_void_p), ("ldx", C.c_int64), ("z", C.c_void_p), ("ldz", C.c_int64),
+                ("w_post", C.c_void_p), ("b_post", C.c_void_p), ("w_pre", C.c_void_p), ("b_pre", C.c_void_p),
+                ("gate", C.c_void_p), ("ldg", C.c_int64), ("gate_kind", C.c_int), ("gate_act", C.c_int),
+                ("h", C.c_void_p), ("ldh", C.c_int64), ("stats_z", C.c_void_p), ("stats_h", C.c_void_p),
+                ("y", C.c_void_p), ("ldy", C.c_int64), ("y8", C.c_void_p), ("ldy8", C.c_int64),
+                ("y8_format", C.c_int), ("y8_scaling", C.c_int),
+                ("y8_scale", C.c_void_p), ("y8_scale_inv", C.c_void_p), ("y8_amax", C.c_void_p)]
+
+
+class NormBwdArgs(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64),
+                ("kind", C.c_int), ("stream_dtype", C.c_int), ("param_dtype", C.c_int),
+                ("res_scale", C.c_float), ("branch_scale", C.c_float),
+                ("dy", C.c_void_p), ("lddy", C.c_int64), ("dh", C.c_void_p), ("lddh", C.c_int64),
+                ("h", C.c_void_p), ("ldh", C.c_int64), ("stats_h", C.c_void_p),
+                ("z", C.c_void_p), ("ldz", C.c_int64), ("stats_z", C.c_void_p),
+                ("w_post", C.c_void_p), ("b_post", C.c_void_p), ("w_pre", C.c_void_p),
+                ("gate", C.c_void_p), ("ldg", C.c_int64), ("gate_kind", C.c_int), ("gate_act", C.c_int),
+                ("dx", C.c_void_p), ("lddx", C.c_int64), ("dz", C.c_void_p), ("lddz", C.c_int64),
+                ("dgate", C.c_void_p), ("lddg", C.c_int64),
+                ("dw_pre", C.c_void_p), ("db_pre", C.c_void_p), ("dw_post", C.c_void_p), ("db_post", C.c_void_p),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
+
+
+class EpilogueArgs(C.Structure):
+    _fields_ = [("backward", C.c_int), ("act", C.c_int), ("param_dtype", C.c_int),
+                ("bias", C.c_void_p), ("residual", C.c_void_p), ("ldres", C.c_int64),
+                ("residual_dtype", C.c_int), ("res_scale", C.c_float),
+                ("aux", C.c_void_p), ("ldaux", C.c_int64), ("dbias", C.c_void_p),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
+
+
+class RopeArgs(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("q_heads", C.c_int64), ("k_heads", C.c_int64),
+                ("dim", C.c_int64), ("pairs", C.c_int64),
+                ("dtype", C.c_int), ("layout", C.c_int), ("inverse", C.c_int), ("scale", C.c_float),
+                ("freqs", C.c_void_p), ("positions", C.c_void_p), ("positions_i64", C.c_int),
+                ("offset", C.c_int64),
+                ("q", C.c_void_p), ("q_token_stride", C.c_int64), ("q_head_stride", C.c_int64),
+                ("k", C.c_void_p), ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64),
+                ("q_out", C.c_void_p), ("q_out_token_stride", C.c_int64), ("q_out_head_stride", C.c_int64),
+                ("k_out", C.c_void_p), ("k_out_token_stride", C.c_int64), ("k_out_head_stride", C.c_int64)]
 
 
 def _load():
@@ -73,6 +128,13 @@ def _load():
         "fp8_cast_sr_state": (i32, [vp, i64, i64, i32, vp, vp, C.c_uint64, vp, vp, vp, vp]),
         "fp8_amax_ewma_update": (i32, [vp, i64, vp, C.c_float, i32, i32, vp, vp, vp]),
         "fp8_scaled_gemm": (i32, [C.POINTER(GemmArgs), vp]),
+        "fp8_block_norm": (i32, [C.POINTER(NormArgs), vp]),
+        "fp8_block_norm_bwd_workspace": (i64, [i64, i64]),
+        "fp8_block_norm_bwd": (i32, [C.POINTER(NormBwdArgs), vp]),
+        "fp8_scaled_gemm_ep_workspace": (i64, [i64, i64, i64, i32, i32]),
+        "fp8_scaled_gemm_ep": (i32, [C.POINTER(GemmArgs), C.POINTER(EpilogueArgs), vp]),
+        "fp8_rope": (i32, [C.POINTER(RopeArgs), vp]),
+        "fp8_rope_freqs": (i32, [vp, i64, C.c_double, i32, C.c_double, C.c_double, C.c_double, C.c_double, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -370,3 +432,263 @@ def fp8_scaled_gemm(A, a_fmt, a_scaling, a_scale_inv, B, b_fmt, b_scaling, b_sca
                  _ptr(d_scale, _F32, "d_scale"), _ptr(D_t, _U8, "D_t"), M,
                  1 if amax_accumulate else 0)
     _check("fp8_scaled_gemm", _L.fp8_scaled_gemm(C.byref(g), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Operators around the linears: norms with the block's gate and residual
+# scale, the GEMM with the linear's epilogue, rotary positions.
+
+_DT = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+_ANY = (torch.bfloat16, torch.float32)
+
+
+def _rows(t, shape, dtypes, name):
+    """(pointer, row stride) of a 2-D GPU tensor of that shape whose rows may
+    be strided; (None, columns) for None."""
+    if t is None:
+        return None, shape[1]
+    if not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a GPU tensor of one of {dtypes}, got {t.dtype} on {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    ld, one = t.stride()
+    if shape[0] <= 1 or shape[1] == 0:
+        ld = shape[1]
+    if (one != 1 and shape[1] > 1) or ld < shape[1]:
+        raise ValueError(f"{name} needs rows of unit stride that do not overlap, got strides {t.stride()}")
+    return t.data_ptr() or None, ld
+
+
+def _vec(t, n, dtype, name):
+    """Pointer of a contiguous 1-D GPU tensor of n elements (None -> NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a GPU tensor of {dtype}, got {t.dtype} on {t.device}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous ({n},) tensor, got {tuple(t.shape)}")
+    return t.data_ptr() or None
+
+
+def _params(n, default, **vectors):
+    """Pointers of [n] parameter vectors of one type, and that type."""
+    kept = [(k, t) for k, t in vectors.items() if t is not None]
+    dtype = kept[0][1].dtype if kept else default
+    if dtype not in _DT:
+        raise TypeError(f"{kept[0][0]} must be bf16 or float32, got {dtype}")
+    return {k: _vec(t, n, dtype, k) for k, t in vectors.items()}, _DT[dtype]
+
+
+def _gate(gate, rows, cols, name="gate"):
+    """(kind, pointer, row stride) of a gate: [cols], [rows, 1] or [rows, cols]."""
+    if gate is None:
+        return GATE_NONE, None, cols
+    if gate.dim() == 1:
+        return GATE_CHANNEL, None, cols   # a parameter: its pointer comes with the others
+    if gate.shape == (rows, 1) and (cols != 1 or gate.dtype == torch.float32):
+        if gate.dtype != torch.float32 or not gate.is_cuda or not gate.is_contiguous():
+            raise TypeError(f"a per-token {name} must be a contiguous float32 GPU tensor")
+        return GATE_TOKEN, gate.data_ptr() or None, cols
+    return (GATE_FULL, *_rows(gate, torch.Size((rows, cols)), _BF16, name))
+
+
+def _workspace(ws, n, like, stream):
+    """(pointer, bytes) of the caller's workspace, or of one from torch's
+    allocator (on the current stream only, whose order keeps it alive)."""
+    if ws is None:
+        if stream is not None:
+            raise ValueError("a call on an explicit stream needs a workspace")
+        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+    elif not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    return ws, ws.data_ptr() or None, ws.numel() * ws.element_size()
+
+
+def fp8_block_norm(x, z=None, h=None, y=None, kind=NORM_RMS, eps=1e-6, w_pre=None, b_pre=None,
+                   w_post=None, b_post=None, gate=None, gate_act=GATE_LINEAR, res_scale=1.0,
+                   branch_scale=1.0, stats_z=None, stats_h=None, y8=None, y8_fmt=E4M3,
+                   y8_scaling=SCALE_TENSOR, y8_scale=None, y8_scale_inv=None, y8_amax=None, stream=None):
+    """h = res_scale * x + branch_scale * gate * N(z), y = N(h), row by row.
+
+    x [rows][cols], bf16 or float32, is the residual stream, z [rows][cols]
+    bf16 the output of the block that ends here (None: h is x), h the new
+    stream (x's type; may be x).  y is bf16; y8 holds FP8 codes of y with
+    y8_scaling SCALE_TENSOR (y8_scale given, y8_amax max-accumulated),
+    SCALE_ROW or SCALE_1x128 (y8_scale_inv written).  Weights and biases [cols]
+    and a per-channel gate [cols] share one type; a gate [rows, 1] is float32, a
+    gate [rows, cols] bf16.  stats_z / stats_h [rows, 2] float32 receive (mean,
+    1 / deviation) for fp8_block_norm_bwd."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
+    shape = x.shape
+    rows, cols = shape
+    xp, ldx = _rows(x, shape, _ANY, "x")
+    zp, ldz = _rows(z, shape, _BF16, "z")
+    hp, ldh = _rows(h, shape, (x.dtype,), "h")
+    yp, ldy = _rows(y, shape, _BF16, "y")
+    y8p, ldy8 = _rows(y8, shape, _U8, "y8")
+    gk, gp, ldg = _gate(gate, rows, cols)
+    v, pt = _params(cols, torch.float32, w_pre=w_pre, b_pre=b_pre, w_post=w_post, b_post=b_post,
+                    gate=gate if gk == GATE_CHANNEL else None)
+    if y8 is not None:
+        if y8_scaling == SCALE_TENSOR:
+            _need(y8_scale, 1, "y8_scale")
+            _need(y8_amax, 1, "y8_amax")
+        else:
+            _need(y8_scale_inv, rows if y8_scaling == SCALE_ROW else (cols + 127) // 128 * rows, "y8_scale_inv")
+    _need(stats_z, 2 * rows, "stats_z")
+    _need(stats_h, 2 * rows, "stats_h")
+    a = NormArgs(rows, cols, kind, _DT[x.dtype], pt, eps, res_scale, branch_scale, xp, ldx, zp, ldz,
+                 v["w_post"], v["b_post"], v["w_pre"], v["b_pre"], v["gate"] if gk == GATE_CHANNEL else gp, ldg, gk,
+                 gate_act, hp, ldh, _ptr(stats_z, _F32, "stats_z"), _ptr(stats_h, _F32, "stats_h"), yp, ldy,
+                 y8p, ldy8, y8_fmt, y8_scaling, _ptr(y8_scale, _F32, "y8_scale"),
+                 _ptr(y8_scale_inv, _F32, "y8_scale_inv"), _ptr(y8_amax, _F32, "y8_amax"))
+    _check("fp8_block_norm", _L.fp8_block_norm(C.byref(a), _stream(stream)))
+
+
+def fp8_block_norm_bwd_workspace(rows, cols) -> int:
+    """Bytes of workspace that fp8_block_norm_bwd needs."""
+    return _L.fp8_block_norm_bwd_workspace(rows, cols)
+
+
+def fp8_block_norm_bwd(h, dx, dy=None, dh=None, z=None, dz=None, kind=NORM_RMS, w_pre=None, w_post=None,
+                       b_post=None, gate=None, gate_act=GATE_LINEAR, res_scale=1.0, branch_scale=1.0,
+                       stats_z=None, stats_h=None, dw_pre=None, db_pre=None, dw_post=None, db_post=None,
+                       dgate=None, workspace=None, stream=None):
+    """Gradients of fp8_block_norm: of x (dx), z (dz), the weights, biases and
+    the gate, from dy (of y; None: y was not made) and dh (what reaches h from
+    above; None: nothing).  h, z and the statistics are the forward call's (h:
+    x where there was no z).  Every output but dx may be left out; dx may be dh
+    and dz may be dy."""
+    if h.dim() != 2:
+        raise ValueError(f"h must be 2-D, got {tuple(h.shape)}")
+    shape = h.shape
+    rows, cols = shape
+    hp, ldh = _rows(h, shape, _ANY, "h")
+    dxp, lddx = _rows(dx, shape, (h.dtype,), "dx")
+    dyp, lddy = _rows(dy, shape, _BF16, "dy")
+    dhp, lddh = _rows(dh, shape, (h.dtype,), "dh")
+    zp, ldz = _rows(z, shape, _BF16, "z")
+    dzp, lddz = _rows(dz, shape, _BF16, "dz")
+    gk, gp, ldg = _gate(gate, rows, cols)
+    dgp, lddg = None, cols
+    channel = gk == GATE_CHANNEL
+    if dgate is not None:
+        if gate is None or dgate.shape != gate.shape or dgate.dtype != gate.dtype:
+            raise ValueError("dgate must have the gate's shape and type")
+        if not channel:
+            _, dgp, lddg = _gate(dgate, rows, cols, "dgate")
+    v, pt = _params(cols, torch.float32, w_pre=w_pre, w_post=w_post, b_post=b_post,
+                    gate=gate if channel else None, dgate=dgate if channel else None,
+                    dw_pre=dw_pre, db_pre=db_pre, dw_post=dw_post, db_post=db_post)
+    _need(stats_z, 2 * rows, "stats_z")
+    _need(stats_h, 2 * rows, "stats_h")
+    ws, wp, wn = _workspace(workspace, _L.fp8_block_norm_bwd_workspace(rows, cols) if workspace is None else 0, h,
+                            stream)
+    a = NormBwdArgs(rows, cols, kind, _DT[h.dtype], pt, res_scale, branch_scale, dyp, lddy, dhp, lddh, hp, ldh,
+                    _ptr(stats_h, _F32, "stats_h"), zp, ldz, _ptr(stats_z, _F32, "stats_z"), v["w_post"],
+                    v["b_post"], v["w_pre"], v["gate"] if channel else gp, ldg, gk, gate_act, dxp, lddx, dzp, lddz,
+                    v["dgate"] if channel else dgp, lddg, v["dw_pre"], v["db_pre"], v["dw_post"], v["db_post"],
+                    wp, wn)
+    _check("fp8_block_norm_bwd", _L.fp8_block_norm_bwd(C.byref(a), _stream(stream)))
+
+
+def fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling) -> int:
+    """Bytes of workspace that fp8_scaled_gemm_ep needs."""
+    return _L.fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling)
+
+
+def fp8_scaled_gemm_ep(A, a_fmt, a_scaling, a_scale_inv, B, b_fmt, b_scaling, b_scale_inv, D, bias=None,
+                       act=ACT_NONE, aux=None, residual=None, res_scale=1.0, backward=False, dbias=None,
+                       d_amax=None, stream=None, d_scale=None, d_fmt=None, D_t=None, amax_accumulate=False,
+                       workspace=None):
+    """fp8_scaled_gemm with the linear's epilogue.  With v the dequantised
+    product: forward, u = v + bias, aux = bf16(u) if given, D = act(u) +
+    res_scale * residual; backward, D = v * act'(aux) and dbias = column sums
+    of it.  D is bf16, float32, or FP8 codes (uint8 or float8; d_fmt, d_scale,
+    optional transposed D_t).  A, B, D, D_t, aux and residual may have strided
+    rows; bias and dbias are [N] bf16 or float32."""
+    M, K = A.shape
+    N = B.shape[0]
+    ap, lda = _rows(A, A.shape, _U8, "A")
+    bp, ldb = _rows(B, torch.Size((N, K)), _U8, "B")
+    mn = torch.Size((M, N))
+    if D.dtype in _U8:
+        if d_fmt not in (E4M3, E5M2):
+            raise ValueError("an FP8 output needs d_fmt (E4M3 or E5M2)")
+        d_dtype = OUT_E4M3 if d_fmt == E4M3 else OUT_E5M2
+    else:
+        d_dtype = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}[D.dtype]
+    dp, ldd = _rows(D, mn, (D.dtype,), "D")
+    tp, ldt = _rows(D_t, torch.Size((N, M)), _U8, "D_t")
+    xp, ldaux = _rows(aux, mn, _BF16, "aux")
+    rp, ldres = _rows(residual, mn, _ANY, "residual")
+    v, pt = _params(N, torch.float32, bias=bias, dbias=dbias)
+    nkb = (K + 127) // 128
+    for s, scaling, rows, name in ((a_scale_inv, a_scaling, M, "a_scale_inv"), (b_scale_inv, b_scaling, N, "b_scale_inv")):
+        if M > 0 and N > 0 and K > 0:
+            _need(s, 1 if scaling == SCALE_TENSOR else rows if scaling == SCALE_ROW else
+                  nkb * (rows if scaling in (SCALE_1x128, SCALE_1x128_POW2) else (rows + 127) // 128), name)
+    _need(d_amax, 1, "d_amax")
+    _need(d_scale, 1, "d_scale")
+    ws, wp, wn = _workspace(workspace, _L.fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling)
+                            if workspace is None else 0, A, stream)
+    g = GemmArgs(M, N, K, lda, ldb, ldd, ap, a_fmt, a_scaling, _ptr(a_scale_inv, _F32, "a_scale_inv"),
+                 bp, b_fmt, b_scaling, _ptr(b_scale_inv, _F32, "b_scale_inv"), dp, d_dtype,
+                 _ptr(d_amax, _F32, "d_amax"), 0, _ptr(d_scale, _F32, "d_scale"), tp, ldt,
+                 1 if amax_accumulate else 0)
+    e = EpilogueArgs(1 if backward else 0, act, pt, v["bias"], rp, ldres,
+                     DT_BF16 if residual is None else _DT[residual.dtype], res_scale, xp, ldaux, v["dbias"], wp, wn)
+    _check("fp8_scaled_gemm_ep", _L.fp8_scaled_gemm_ep(C.byref(g), C.byref(e), _stream(stream)))
+
+
+def fp8_rope_freqs(freqs, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, trained=8192.0, low=1.0, high=32.0,
+                   stream=None):
+    """Rotation frequencies of freqs.numel() pairs (a float64 GPU tensor, filled
+    here): base^(-i / pairs), scaled for contexts beyond the trained length by
+    `scaling` (ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS)."""
+    _check("fp8_rope_freqs",
+           _L.fp8_rope_freqs(_ptr(freqs, (torch.float64,), "freqs"), freqs.numel(), base, scaling, factor, trained,
+                             low, high, _stream(stream)))
+
+
+def _heads(t, tokens, dim, dtype, name):
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a GPU tensor of {dtype}, got {t.dtype} on {t.device}")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim or (dim > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [{tokens}][heads][{dim}] with unit stride inside a head, got "
+                         f"{tuple(t.shape)}, strides {t.stride()}")
+    return t.shape[1], t.data_ptr() or None, t.stride(0), t.stride(1)
+
+
+def fp8_rope(q, freqs, positions=None, k=None, q_out=None, k_out=None, layout=ROPE_HALF, inverse=False,
+             scale=1.0, offset=0, stream=None):
+    """Turns pair i of every head of q (and k) [tokens][heads][dim] by
+    (position + offset) * freqs[i] and scales it; elements past the 2 *
+    freqs.numel() turned ones are copied.  q and k may be strided views of one
+    QKV tensor; without q_out / k_out they are turned in place.  positions:
+    [tokens] int32 or int64 (None: 0, 1, ...).  inverse=True turns back: the
+    gradient."""
+    tokens, _, dim = q.shape
+    qh, qp, qs, qhs = _heads(q, tokens, dim, q.dtype if q.dtype in _DT else torch.bfloat16, "q")
+    qo = q if q_out is None else q_out
+    qoh, qop, qos, qohs = _heads(qo, tokens, dim, q.dtype, "q_out")
+    kh, kp, ks, khs, kop, kos, kohs = 0, None, 0, 0, None, 0, 0
+    if k is not None:
+        kh, kp, ks, khs = _heads(k, tokens, dim, q.dtype, "k")
+        koh, kop, kos, kohs = _heads(k if k_out is None else k_out, tokens, dim, q.dtype, "k_out")
+        if koh != kh:
+            raise ValueError("k_out must have k's heads")
+    if qoh != qh:
+        raise ValueError("q_out must have q's heads")
+    pp, wide = None, 0
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+        if positions.shape != (tokens,):
+            raise ValueError(f"positions must be ({tokens},), got {tuple(positions.shape)}")
+        pp, wide = _ptr(positions, None, "positions"), 1 if positions.dtype == torch.int64 else 0
+    a = RopeArgs(tokens, qh, kh, dim, freqs.numel(), _DT[q.dtype], layout, 1 if inverse else 0, scale,
+                 _ptr(freqs, (torch.float64,), "freqs"), pp, wide, offset, qp, qs, qhs, kp, ks, khs,
+                 qop, qos, qohs, kop, kos, kohs)
+    _check("fp8_rope", _L.fp8_rope(C.byref(a), _stream(stream)))

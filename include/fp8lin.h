@@ -462,6 +462,227 @@ typedef struct {
 
 fp8_status fp8_scaled_gemm(const fp8_gemm_args* args, hipStream_t stream);
 
+/* ========================================================================
+ * The operators around the linears of a transformer block: norms with the
+ * block's gate and residual scale, the GEMM with the linear's bias,
+ * activation and residual, and rotary positions, each with its gradient.
+ * They were added without changing any structure above, so the ABI version
+ * stays.  Beyond the conventions at the top:
+ *   - rows may be strided (ld >= columns, in elements); pointers need the
+ *     alignment of their element only, unless stated otherwise;
+ *   - an optional output or input is NULL when absent;
+ *   - parameters (weights, biases, a per-channel gate) and their gradients
+ *     have one type per call, param_dtype;
+ *   - a workspace is caller-owned device memory, 16-byte aligned, that the
+ *     call may overwrite; its contents mean nothing afterwards.  Calls that
+ *     may overlap need one each.
+ * Every sum, norm statistic and column sum is held in binary32 and taken in
+ * a fixed order: equal inputs on equal hardware give equal bits.
+ * ===================================================================== */
+typedef enum { FP8_DT_BF16 = 0, FP8_DT_F32 = 1 } fp8_dtype;
+typedef enum { FP8_NORM_RMS = 0, FP8_NORM_LAYER = 1 } fp8_norm_kind;
+/* Gate of a block's output: none, one value per channel [cols]
+ * (param_dtype), per token [rows] (FP32), or per element [rows][ldg] (BF16);
+ * used as it is, or through a sigmoid or a hyperbolic tangent. */
+typedef enum {
+  FP8_GATE_NONE = 0, FP8_GATE_CHANNEL = 1, FP8_GATE_TOKEN = 2, FP8_GATE_FULL = 3
+} fp8_gate_kind;
+typedef enum { FP8_GATE_LINEAR = 0, FP8_GATE_SIGMOID = 1, FP8_GATE_TANH = 2 } fp8_gate_act;
+
+/* ------------------------------------------------------------------------
+ * fp8_block_norm -- per row of `cols` values, with N the norm of `kind`:
+ *   h = res_scale * x + branch_scale * G(gate) * (N(z) * w_post + b_post)
+ *   y = N(h) * w_pre + b_pre,   N(v) = (v - mean) * rstd,
+ *   rstd = 1 / sqrt(mean((v - mean)^2) + eps), mean taken as 0 for the RMS
+ *   norm.
+ *   x       [rows][ldx], stream_dtype: the residual stream.
+ *   z       [rows][ldz] BF16: the block's output.  NULL: no block ends here,
+ *           h is x itself (res_scale unused) and `h` must be NULL.
+ *   h       [rows][ldh], stream_dtype: the new stream; may be x in place.
+ *   w_post, b_post, w_pre, b_pre  [cols]; NULL weight: 1, NULL bias: 0.  Biases
+ *           belong to the layer norm only.
+ *   stats_z, stats_h  [rows][2] FP32 (mean, rstd), for the gradient.
+ *   y       [rows][ldy] BF16, and / or
+ *   y8      [rows][ldy8] FP8 codes of y (of its binary32 value), y8_format,
+ *           with y8_scaling
+ *             FP8_SCALE_TENSOR: y8_scale (1 float) as in fp8_cast_e4m3 /
+ *               e5m2; y8_amax (1 float, optional) is max-accumulated with
+ *               max |y| as in fp8_amax_acc;
+ *             FP8_SCALE_ROW: the row's own scale, y8_scale_inv [rows], as
+ *               fp8_cast_rowwise;
+ *             FP8_SCALE_1x128: y8_scale_inv [ceil(cols/128)][rows], as
+ *               fp8_cast_block.
+ *   With neither y nor y8 only h is made (then z is required).
+ * y is taken from h in binary32, before h is rounded to stream_dtype.  No
+ * other output may overlap an input.
+ * Errors: FP8_ERR_NULL (args, x, h with z, a scale), FP8_ERR_SHAPE (negative
+ * size, ld < cols), FP8_ERR_ARG (an enum, eps negative or NaN, h without z, a
+ * gate without z or unlike gate_kind, a bias with the RMS norm, nothing to
+ * make), FP8_ERR_UNSUPPORTED (cols > 32768; y8_scaling), FP8_ERR_ALIGN.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int64_t rows, cols;
+  fp8_norm_kind kind;
+  fp8_dtype stream_dtype, param_dtype;
+  float eps, res_scale, branch_scale;
+  const void* x; int64_t ldx;
+  const void* z; int64_t ldz;
+  const void* w_post; const void* b_post; const void* w_pre; const void* b_pre;
+  const void* gate; int64_t ldg; fp8_gate_kind gate_kind; fp8_gate_act gate_act;
+  void* h; int64_t ldh;
+  float* stats_z; float* stats_h;
+  void* y; int64_t ldy;
+  uint8_t* y8; int64_t ldy8; fp8_format y8_format; fp8_scaling y8_scaling;
+  const float* y8_scale; float* y8_scale_inv; float* y8_amax;
+} fp8_norm_args;
+
+fp8_status fp8_block_norm(const fp8_norm_args* args, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_block_norm_bwd -- gradients of fp8_block_norm.
+ *   dy       [rows][lddy] BF16: gradient of y (of the values that y8 stands
+ *            for); NULL: y was not made.
+ *   dh       [rows][lddh] stream_dtype: gradient that reaches h from above;
+ *            NULL: 0.
+ *   h, stats_h  as written by the forward pass (h: x where there was no z);
+ *            needed with dy.   z, stats_z, w_post, gate: as given to it;
+ *            needed where there was a z.  b_post only for dgate.
+ *   dx       [rows][lddx] stream_dtype, may be dh in place;  dz [rows][lddz]
+ *            BF16, may be dy in place;  dgate: gate's shape and type ([rows][lddg]
+ *            for FP8_GATE_FULL);  dw_pre, db_pre, dw_post, db_post [cols],
+ *            param_dtype: overwritten.
+ *   Each output is optional.  rows == 0 sets the column sums to 0.
+ *   workspace  fp8_block_norm_bwd_workspace(rows, cols) bytes.
+ * Errors: as fp8_block_norm; FP8_ERR_NULL also for the workspace,
+ * FP8_ERR_SHAPE for one that is too small, FP8_ERR_ARG for an output whose
+ * input is missing.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int64_t rows, cols;
+  fp8_norm_kind kind;
+  fp8_dtype stream_dtype, param_dtype;
+  float res_scale, branch_scale;
+  const void* dy; int64_t lddy;
+  const void* dh; int64_t lddh;
+  const void* h; int64_t ldh; const float* stats_h;
+  const void* z; int64_t ldz; const float* stats_z;
+  const void* w_post; const void* b_post; const void* w_pre;
+  const void* gate; int64_t ldg; fp8_gate_kind gate_kind; fp8_gate_act gate_act;
+  void* dx; int64_t lddx;
+  void* dz; int64_t lddz;
+  void* dgate; int64_t lddg;
+  void* dw_pre; void* db_pre; void* dw_post; void* db_post;
+  void* workspace; int64_t workspace_bytes;
+} fp8_norm_bwd_args;
+
+int64_t fp8_block_norm_bwd_workspace(int64_t rows, int64_t cols);
+fp8_status fp8_block_norm_bwd(const fp8_norm_bwd_args* args, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_scaled_gemm_ep -- fp8_scaled_gemm with the linear's epilogue.  With v
+ * the dequantised product in binary32 (every operand format and scaling of
+ * fp8_scaled_gemm):
+ *   forward  (backward = 0):  u = v + bias[n];  aux[m][n] = bf16(u);
+ *                             d = act(u) + res_scale * residual[m][n]
+ *   backward (backward = 1):  d = v * act'(aux[m][n]);
+ *                             dbias[n] = sum_m d
+ * and D = d in gemm->d_dtype: BF16, FP32, or FP8 codes of d * d_scale with the
+ * transposed copy D_t; d_amax as in fp8_scaled_gemm (max |d|).  The forward
+ * call is a linear with its bias and activation (the next linear's cast in the
+ * same pass, if FP8); the backward call is the dgrad product of the linear
+ * after the activation, and gives the gradient before it: the operand of the
+ * wgrad and dgrad of the linear before.
+ *   bias      [N] param_dtype, optional.   dbias [N] param_dtype, optional.
+ *   act       FP8_ACT_GELU_TANH is the tanh form of GELU.
+ *   aux       [M][ldaux] BF16.  Forward: optional output, the pre-activation.
+ *             Backward: input, required unless act is FP8_ACT_NONE.
+ *   residual  [M][ldres] residual_dtype, optional; may be D in place if the
+ *             types agree.
+ *   workspace fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling)
+ *             bytes.
+ * Shape rules, scalings and errors as fp8_scaled_gemm, and: FP8_ERR_ARG (act,
+ * dtypes, bias or residual in a backward call, dbias in a forward one),
+ * FP8_ERR_NULL (aux of a backward call, workspace), FP8_ERR_SHAPE (ldaux,
+ * ldres < N, a workspace that is too small), FP8_ERR_UNSUPPORTED (gemm's
+ * accumulate; 256 * lda or 256 * ldb >= 2^31).
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  FP8_ACT_NONE = 0, FP8_ACT_RELU = 1, FP8_ACT_GELU = 2, FP8_ACT_GELU_TANH = 3, FP8_ACT_SILU = 4
+} fp8_activation;
+
+typedef struct {
+  int backward;
+  fp8_activation act;
+  fp8_dtype param_dtype;
+  const void* bias;
+  const void* residual; int64_t ldres; fp8_dtype residual_dtype; float res_scale;
+  void* aux; int64_t ldaux;
+  void* dbias;
+  void* workspace; int64_t workspace_bytes;
+} fp8_epilogue_args;
+
+int64_t fp8_scaled_gemm_ep_workspace(int64_t M, int64_t N, int64_t K, fp8_scaling a_scaling,
+                                     fp8_scaling b_scaling);
+fp8_status fp8_scaled_gemm_ep(const fp8_gemm_args* gemm, const fp8_epilogue_args* ep,
+                              hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_rope -- rotary positions of the query and key heads of a QKV product.
+ * Pair i < pairs of a head is (i, i + pairs) (FP8_ROPE_HALF) or (2i, 2i + 1)
+ * (FP8_ROPE_INTERLEAVED); with theta = (position + offset) * freqs[i], reduced
+ * in binary64,
+ *   (x0, x1) -> scale * (x0 cos - x1 sin, x1 cos + x0 sin),
+ * and elements 2 * pairs .. dim - 1 are copied.  inverse = 1 turns by -theta:
+ * the gradient of the call with inverse = 0.
+ *   q, k          [tokens][heads][dim] in dtype: unit stride inside a head,
+ *                 strides of tokens and heads in elements (views of one QKV
+ *                 tensor, for instance); k NULL: no key heads.
+ *   q_out, k_out  the same shapes, strides of their own; may be q, k in place
+ *                 (same pointer and strides), else no overlap.
+ *   positions     [tokens] int32 or int64 (positions_i64); NULL: 0, 1, ...
+ *   offset        added to every position.
+ *   freqs         [pairs] binary64, as fp8_rope_freqs makes them.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (negative sizes, 2 * pairs > dim),
+ * FP8_ERR_ARG (enums), FP8_ERR_ALIGN, FP8_ERR_UNSUPPORTED (pairs > 1024, dim,
+ * q_heads + k_heads > 65535, tokens > 2^23).
+ * ---------------------------------------------------------------------- */
+typedef enum { FP8_ROPE_HALF = 0, FP8_ROPE_INTERLEAVED = 1 } fp8_rope_layout;
+
+typedef struct {
+  int64_t tokens, q_heads, k_heads, dim, pairs;
+  fp8_dtype dtype; fp8_rope_layout layout;
+  int inverse;
+  float scale;
+  const double* freqs;
+  const void* positions; int positions_i64; int64_t offset;
+  const void* q; int64_t q_token_stride, q_head_stride;
+  const void* k; int64_t k_token_stride, k_head_stride;
+  void* q_out; int64_t q_out_token_stride, q_out_head_stride;
+  void* k_out; int64_t k_out_token_stride, k_out_head_stride;
+} fp8_rope_args;
+
+fp8_status fp8_rope(const fp8_rope_args* args, hipStream_t stream);
+
+/* fp8_rope_freqs -- the frequencies, once per model: freqs[i] = base^(-i /
+ * pairs), i < pairs, scaled for contexts beyond the trained length:
+ *   FP8_ROPE_PLAIN   as they are;
+ *   FP8_ROPE_LINEAR  divided by factor (positions interpolated);
+ *   FP8_ROPE_BASE    base replaced by base * factor^(pairs / (pairs - 1)): the
+ *                    fastest pair is left, the slowest divided by factor;
+ *   FP8_ROPE_PARTS   f keep + f / factor (1 - keep), keep = clamp((trained f /
+ *                    (2 pi) - low) / (high - low), 0, 1): pairs that turn
+ *                    more than `high` times over the trained length are left,
+ *                    those that turn less than `low` times interpolated.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (pairs < 0), FP8_ERR_ALIGN, FP8_ERR_ARG
+ * (enum; base, factor or trained not positive and finite; high <= low). */
+typedef enum {
+  FP8_ROPE_PLAIN = 0, FP8_ROPE_LINEAR = 1, FP8_ROPE_BASE = 2, FP8_ROPE_PARTS = 3
+} fp8_rope_scaling;
+
+fp8_status fp8_rope_freqs(double* freqs, int64_t pairs, double base, fp8_rope_scaling scaling,
+                          double factor, double trained, double low, double high,
+                          hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
