@@ -84,7 +84,7 @@ fp8_status fp8_block_norm(const fp8_norm_args* args, hipStream_t stream) {
 
 int64_t fp8_block_norm_bwd_workspace(int64_t rows, int64_t cols) {
   if (rows < 0 || cols <= 0) return 0;
-  return 4 * norm_parts(rows) * cols * (int64_t)sizeof(float);
+  return 4 * norm_parts(rows, cols) * cols * (int64_t)sizeof(float);
 }
 
 fp8_status fp8_block_norm_bwd(const fp8_norm_bwd_args* args, hipStream_t stream) {

@@ -150,10 +150,10 @@ struct NormGradParams {
   void *dgate;
   int64_t lddg;
   void *dw_pre, *db_pre, *dw_post, *db_post;
-  float* part;   // workspace: 4 * norm_parts(rows) * cols floats
+  float* part;   // workspace: 4 * norm_parts(rows, cols) * cols floats
 };
 int64_t norm_max_cols();
-int64_t norm_parts(int64_t rows);
+int64_t norm_parts(int64_t rows, int64_t cols);
 hipError_t launch_norm_fwd(const NormParams& p, hipStream_t s);
 hipError_t launch_norm_bwd(const NormGradParams& p, hipStream_t s);
 

@@ -27,11 +27,57 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_op));
 }
 
+// ---- rows cut into vectors of eight, one per lane, for loads that are issued
+// long before they are used.  Vector v of a row of `cols` elements starts at 8 v;
+// the last one, if cols is no multiple of 8, starts at cols - 8, so that it is one
+// 16-byte load like the others and needs no wait for what is in flight, and its
+// first `skip` elements belong to the vector before: they are left out of sums
+// and stores.  (Read element by element, the last vector waited for every load
+// before it, and with it the whole workgroup: BF16 norm of 4096 x 4104, 45 us.)
+// skip = 8: no such vector.  TINY: a row of fewer than 8 elements, whose only
+// vector starts at c < 0 (kernels of their own: the accesses of single elements
+// cost the others some 20 registers).
+struct RowVec {
+  int c, skip;
+  __device__ __forceinline__ RowVec() {}
+  __device__ __forceinline__ RowVec(int cols, int v) {
+    const int left = cols - 8 * v;
+    c = left >= 8 ? 8 * v : cols - 8;
+    skip = left >= 8 ? 0 : (left > 0 ? 8 - left : 8);
+  }
+};
+// Element i of an array.  With a 32-bit index and a base that is the same in all
+// lanes the address is that base plus a 32-bit offset: one register for all the
+// arrays of a row, where 64-bit addresses take two for each.
+template <typename T, typename I>
+__device__ __forceinline__ const T* elem(const void* base, I i) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + (I)(i * (I)sizeof(T)));
+}
+template <typename T, typename I>
+__device__ __forceinline__ T* elem(void* base, I i) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(base) + (I)(i * (I)sizeof(T)));
+}
+
+// Eight bf16 as whole dwords of memory: the four from the dword that holds the
+// first, and, where that one starts in the middle of it, the last element by
+// itself.  (A 16-byte load that does not start on a dword costs several times
+// one that does: BF16 norm of 4096 x 4095, 62 us so, 44 us as here.)
+__device__ __forceinline__ uint32_t odd_of(const void* p) { return (uint32_t)reinterpret_cast<uintptr_t>(p) & 2u; }
+__device__ __forceinline__ void load_dwords(const uint16_t* p, uint32_t (&w)[5]) {
+  const uint32_t o = odd_of(p);
+  const Pk16a4 a = *reinterpret_cast<const Pk16a4*>(reinterpret_cast<const char*>(p) - o);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = a.v[k];
+  w[4] = 0u;
+  if (o) w[4] = p[7];
+}
+
 // v[0..7] = elements i .. i+7 of a bf16 (F32 = 0) or binary32 (F32 = 1) array;
 // n < 8: only the first n are there, the others become 0.
-__device__ __forceinline__ void load8(const void* base, int f32, int64_t i, int n, float (&v)[8]) {
+template <typename I>
+__device__ __forceinline__ void load8(const void* base, int f32, I i, int n, float (&v)[8]) {
   if (f32) {
-    const float* p = reinterpret_cast<const float*>(base) + i;
+    const float* p = elem<float>(base, i);
     if (n >= 8) {
       const Pk16a4 a = *reinterpret_cast<const Pk16a4*>(p);
       const Pk16a4 b = *reinterpret_cast<const Pk16a4*>(p + 4);
@@ -45,13 +91,16 @@ __device__ __forceinline__ void load8(const void* base, int f32, int64_t i, int 
       for (int k = 0; k < 8; ++k) v[k] = k < n ? p[k] : 0.0f;
     }
   } else {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + i;
+    const uint16_t* p = elem<uint16_t>(base, i);
     if (n >= 8) {
-      const Pk16a2 a = *reinterpret_cast<const Pk16a2*>(p);
+      uint32_t w[5];
+      load_dwords(p, w);
+      const uint32_t o = odd_of(p);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        v[2 * k] = bf16_lo(a.v[k]);
-        v[2 * k + 1] = bf16_hi(a.v[k]);
+        const uint32_t d = __builtin_amdgcn_alignbyte(w[k + 1], w[k], o);
+        v[2 * k] = bf16_lo(d);
+        v[2 * k + 1] = bf16_hi(d);
       }
     } else {
 #pragma unroll
@@ -60,9 +109,10 @@ __device__ __forceinline__ void load8(const void* base, int f32, int64_t i, int 
   }
 }
 
-__device__ __forceinline__ void store8(void* base, int f32, int64_t i, int n, const float (&v)[8]) {
+template <typename I>
+__device__ __forceinline__ void store8(void* base, int f32, I i, int n, const float (&v)[8]) {
   if (f32) {
-    float* p = reinterpret_cast<float*>(base) + i;
+    float* p = elem<float>(base, i);
     if (n >= 8) {
       Pk16a4 a, b;
 #pragma unroll
@@ -78,7 +128,7 @@ __device__ __forceinline__ void store8(void* base, int f32, int64_t i, int n, co
         if (k < n) p[k] = v[k];
     }
   } else {
-    uint16_t* p = reinterpret_cast<uint16_t*>(base) + i;
+    uint16_t* p = elem<uint16_t>(base, i);
     Pk16a2 a;
 #pragma unroll
     for (int k = 0; k < 4; ++k) a.v[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
@@ -88,6 +138,64 @@ __device__ __forceinline__ void store8(void* base, int f32, int64_t i, int n, co
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k < n) p[k] = (uint16_t)(a.v[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+}
+
+// As the elements lie in memory: a bf16 vector waits in five registers, not in
+// eight.
+template <bool F32>
+struct Raw8 {
+  uint32_t v[F32 ? 8 : 5];
+};
+template <bool F32, bool TINY>
+__device__ __forceinline__ Raw8<F32> load_raw(const void* row, const RowVec& x) {
+  Raw8<F32> r;
+#pragma unroll
+  for (int k = 0; k < (F32 ? 8 : 5); ++k) r.v[k] = 0u;
+  if (x.skip >= 8) return r;
+  if constexpr (!TINY) {
+    if constexpr (F32) {
+      const float* p = elem<float>(row, (uint32_t)x.c);
+      const Pk16a4 a = *reinterpret_cast<const Pk16a4*>(p);
+      const Pk16a4 b = *reinterpret_cast<const Pk16a4*>(p + 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        r.v[k] = a.v[k];
+        r.v[k + 4] = b.v[k];
+      }
+    } else {
+      load_dwords(elem<uint16_t>(row, (uint32_t)x.c), r.v);
+    }
+  } else if constexpr (F32) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k >= x.skip) r.v[k] = __float_as_uint(reinterpret_cast<const float*>(row)[x.c + k]);
+  } else {
+    uint32_t d[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k >= x.skip) d[k >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[x.c + k] << (16 * (k & 1));
+    const bool o = ((odd_of(row) ^ (2u * (uint32_t)x.c)) & 2u) != 0u;
+    r.v[0] = o ? d[0] << 16 : d[0];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) r.v[k] = o ? __builtin_amdgcn_alignbyte(d[k], d[k - 1], 2) : d[k];
+    r.v[4] = d[3] >> 16;
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack(const Raw8<F32>& r, const void* row, const RowVec& x, float (&v)[8]) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r.v[k]);
+  } else {
+    const uint32_t o = (odd_of(row) ^ (2u * (uint32_t)x.c)) & 2u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t d = __builtin_amdgcn_alignbyte(r.v[k + 1], r.v[k], o);
+      v[2 * k] = bf16_lo(d);
+      v[2 * k + 1] = bf16_hi(d);
     }
   }
 }
@@ -144,6 +252,98 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
 __device__ __forceinline__ uint32_t lane_u32(uint32_t v, int lane) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
+// The value of the lane before / after in a row of 16 lanes (0 at its ends).
+__device__ __forceinline__ uint32_t lane_before(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);   // row_shr:1
+}
+__device__ __forceinline__ uint32_t lane_after(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x101, 0xF, 0xF, true);   // row_shl:1
+}
+
+// NW dwords per lane to byte address p, where SEG neighbouring lanes (SEG
+// divides 16, and the group starts at a multiple of it) write one after the
+// other into one row; every lane of the wavefront calls it, `full` for those
+// that have a whole vector.  A vector that does not start on a dword costs
+// several times an aligned one, so such a row is written as the dwords of memory: each lane takes the
+// bytes that its first dword shares with the lane before, and only the ends of a
+// group write single bytes.
+template <int NW, int SEG>
+__device__ __forceinline__ void store_row(uint8_t* p, const uint32_t (&w)[NW], bool full) {
+  struct __attribute__((packed, aligned(4))) Words { uint32_t v[NW]; };
+  struct __attribute__((packed, aligned(4))) Rest { uint32_t v[NW - 1]; };
+  const uint32_t o = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3u);
+  if (__builtin_expect(__any(o != 0 && full), 0)) {
+    const int at = (int)(threadIdx.x & (SEG - 1));
+    // (every lane takes part in each exchange: none inside a short-circuit)
+    const uint32_t f = full ? 1u : 0u, carry = lane_before(w[NW - 1]), fb = lane_before(f), fa = lane_after(f);
+    const bool before = (at != 0) & (fb != 0u), after = (at != SEG - 1) & (fa != 0u);
+    if (!full) return;
+    Words a;
+    a.v[0] = o == 0 ? w[0] : __builtin_amdgcn_alignbyte(w[0], carry, 4 - o);
+#pragma unroll
+    for (int k = 1; k < NW; ++k) a.v[k] = o == 0 ? w[k] : __builtin_amdgcn_alignbyte(w[k], w[k - 1], 4 - o);
+    if (o == 0 || before) {
+      *reinterpret_cast<Words*>(p - o) = a;
+    } else {
+      Rest r;
+#pragma unroll
+      for (int k = 1; k < NW; ++k) r.v[k - 1] = a.v[k];
+      *reinterpret_cast<Rest*>(p - o + 4) = r;
+      for (uint32_t b = 0; b < 4 - o; ++b) p[b] = (uint8_t)(w[0] >> (8 * b));
+    }
+    if (o != 0 && !after)
+      for (uint32_t b = 4 - o; b < 4; ++b) p[4 * (NW - 1) + b] = (uint8_t)(w[NW - 1] >> (8 * b));
+    return;
+  }
+  if (full) {
+    Words a;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) a.v[k] = w[k];
+    *reinterpret_cast<Words*>(p) = a;
+  }
+}
+
+template <bool TINY, typename T>
+__device__ __forceinline__ T* place(void* row, const RowVec& x, int k) {
+  if constexpr (TINY) return reinterpret_cast<T*>(row) + (x.c + k);
+  else return elem<T>(row, (uint32_t)x.c) + k;
+}
+// Eight bf16 or binary32 values, or eight codes, of a row's vector (see store_row
+// and RowVec; every lane of the wavefront calls it).  live: whether to write.
+template <bool TINY>
+__device__ __forceinline__ void store_vec(void* row, int f32, const RowVec& x, bool live, const float (&v)[8]) {
+  if (f32) {
+    if (!live) return;
+    if (x.skip == 0) {
+      store8(row, 1, (uint32_t)x.c, 8, v);
+    } else {
+#pragma unroll
+      for (int k = 1; k < 8; ++k)
+        if (k >= x.skip) *place<TINY, float>(row, x, k) = v[k];
+    }
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+  store_row<4, 16>(reinterpret_cast<uint8_t*>(elem<uint16_t>(row, (uint32_t)x.c)), w, live && x.skip == 0);
+  if (live && x.skip > 0 && x.skip < 8) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+      if (k >= x.skip) *place<TINY, uint16_t>(row, x, k) = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+  }
+}
+template <bool TINY>
+__device__ __forceinline__ void store_vec_codes(uint8_t* row, const RowVec& x, uint32_t lo, uint32_t hi) {
+  const uint32_t w[2] = {lo, hi};
+  store_row<2, 16>(elem<uint8_t>(row, (uint32_t)x.c), w, x.skip == 0);
+  if (x.skip > 0 && x.skip < 8) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+      if (k >= x.skip) *place<TINY, uint8_t>(row, x, k) = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+  }
+}
+
 // Over the 64 lanes, the same in every lane.
 __device__ __forceinline__ float wave_sum(float v) {
   const uint32_t b = __float_as_uint(row16_sum(v));
@@ -157,10 +357,21 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Gate G(g) and its derivative: 0 g itself, 1 sigmoid, 2 tanh.
+constexpr float kLog2E = 1.44269504088896f;
+
+// Gate G(g) and its derivative: 0 g itself, 1 sigmoid, 2 tanh.  With e =
+// exp(-2 |g|), tanh |g| = (1 - e) / (1 + e), which loses bits where 1 - e
+// cancels: below 1/4 the series to g^9 (the next term is below 2^-26 of it).
 __device__ __forceinline__ float gate_value(int act, float g) {
-  if (act == 1) return 1.0f / (1.0f + expf(-g));
-  if (act == 2) return tanhf(g);
+  if (act == 1) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * g));
+  if (act == 2) {
+    const float a = __builtin_fabsf(g), e = __builtin_amdgcn_exp2f(-2.0f * kLog2E * a), q = g * g;
+    const float series = g * __builtin_fmaf(
+        q, __builtin_fmaf(q, __builtin_fmaf(q, __builtin_fmaf(q, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f),
+                          -1.0f / 3.0f), 1.0f);
+    const float far = __builtin_copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), g);
+    return a < 0.25f ? series : far;
+  }
   return g;
 }
 __device__ __forceinline__ float gate_slope(int act, float value) {
@@ -173,7 +384,6 @@ __device__ __forceinline__ float gate_slope(int act, float value) {
 // 3 GELU (tanh form), 4 SiLU.  The sigmoid forms cost one exponential and one
 // reciprocal: the tanh form of GELU is u * sigmoid(2 t), t = sqrt(2/pi) (u +
 // 0.044715 u^3), because 0.5 (1 + tanh t) = sigmoid(2 t).
-constexpr float kLog2E = 1.44269504088896f;
 constexpr float kRootTwoOverPi = 0.797884560802865f;
 __device__ __forceinline__ float sigmoid_of_log2(float t) {   // 1 / (1 + 2^-t)
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-t));

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -128,12 +129,12 @@ def _load():
         "fp8_cast_sr_state": (i32, [vp, i64, i64, i32, vp, vp, C.c_uint64, vp, vp, vp, vp]),
         "fp8_amax_ewma_update": (i32, [vp, i64, vp, C.c_float, i32, i32, vp, vp, vp]),
         "fp8_scaled_gemm": (i32, [C.POINTER(GemmArgs), vp]),
-        "fp8_block_norm": (i32, [C.POINTER(NormArgs), vp]),
+        "fp8_block_norm": (i32, [vp, vp]),
         "fp8_block_norm_bwd_workspace": (i64, [i64, i64]),
-        "fp8_block_norm_bwd": (i32, [C.POINTER(NormBwdArgs), vp]),
+        "fp8_block_norm_bwd": (i32, [vp, vp]),
         "fp8_scaled_gemm_ep_workspace": (i64, [i64, i64, i64, i32, i32]),
-        "fp8_scaled_gemm_ep": (i32, [C.POINTER(GemmArgs), C.POINTER(EpilogueArgs), vp]),
-        "fp8_rope": (i32, [C.POINTER(RopeArgs), vp]),
+        "fp8_scaled_gemm_ep": (i32, [vp, vp, vp]),
+        "fp8_rope": (i32, [vp, vp]),
         "fp8_rope_freqs": (i32, [vp, i64, C.c_double, i32, C.c_double, C.c_double, C.c_double, C.c_double, vp]),
     }
     for name, (res, args) in sig.items():
@@ -174,8 +175,8 @@ def _ptr(t, dtypes=None, name="tensor"):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the handle of torch.cuda.current_stream(), without the object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -437,71 +438,127 @@ def fp8_scaled_gemm(A, a_fmt, a_scaling, a_scale_inv, B, b_fmt, b_scaling, b_sca
 # ---------------------------------------------------------------------------
 # Operators around the linears: norms with the block's gate and residual
 # scale, the GEMM with the linear's epilogue, rotary positions.
+#
+# One token's call is over in less time than a Structure of 30 fields takes to
+# fill, so the argument blocks are packed in one step (the layouts are checked
+# against the Structures below) and each tensor is looked at once.
 
 _DT = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
-_ANY = (torch.bfloat16, torch.float32)
+_BFLOAT, _FLOAT = torch.bfloat16, torch.float32
 
 
-def _rows(t, shape, dtypes, name):
-    """(pointer, row stride) of a 2-D GPU tensor of that shape whose rows may
-    be strided; (None, columns) for None."""
+def _packer(fmt, structure):
+    s = struct.Struct("@" + fmt + "0q")
+    if s.size != C.sizeof(structure):
+        raise ImportError(f"layout of {structure.__name__}: {s.size} bytes packed, {C.sizeof(structure)} declared")
+    return s.pack
+
+
+_pack_gemm = _packer("qqqqqqPiiPPiiPPiPiPPqi", GemmArgs)
+_pack_norm = _packer("qqiiifffPqPqPPPPPqiiPqPPPqPqiiPPP", NormArgs)
+_pack_norm_bwd = _packer("qqiiiffPqPqPqPPqPPPPPqiiPqPqPqPPPPPq", NormBwdArgs)
+_pack_ep = _packer("iiiPPqifPqPPq", EpilogueArgs)
+_pack_rope = _packer("qqqqqiiifPPiqPqqPqqPqqPqq", RopeArgs)
+
+
+def _refuse(t, want, dtype, name):
+    """What is wrong with a tensor that should have been [want] of dtype."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be {tuple(want)} with rows of unit stride that do not overlap, got "
+                     f"{tuple(t.shape)}, strides {t.stride()}")
+
+
+def _mat(t, shape, dtype, name):
+    """(pointer, row stride) of a 2-D GPU tensor of that shape and type, whose
+    rows may be strided; (0, columns) for None."""
     if t is None:
-        return None, shape[1]
-    if not t.is_cuda or t.dtype not in dtypes:
-        raise TypeError(f"{name} must be a GPU tensor of one of {dtypes}, got {t.dtype} on {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        return 0, shape[1]
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda:
+        _refuse(t, shape, dtype, name)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     ld, one = t.stride()
-    if shape[0] <= 1 or shape[1] == 0:
+    if shape[0] == 1:
         ld = shape[1]
     if (one != 1 and shape[1] > 1) or ld < shape[1]:
-        raise ValueError(f"{name} needs rows of unit stride that do not overlap, got strides {t.stride()}")
-    return t.data_ptr() or None, ld
+        _refuse(t, shape, dtype, name)
+    return t.data_ptr(), ld
+
+
+def _codes(t, shape, name):
+    """_mat of FP8 codes (uint8 or a float8 type)."""
+    if t is not None and t.dtype not in _U8:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_U8}")
+    return _mat(t, shape, None if t is None else t.dtype, name)
 
 
 def _vec(t, n, dtype, name):
-    """Pointer of a contiguous 1-D GPU tensor of n elements (None -> NULL)."""
+    """Pointer of a contiguous 1-D GPU tensor of n elements (None -> 0)."""
     if t is None:
-        return None
-    if not t.is_cuda or t.dtype != dtype:
-        raise TypeError(f"{name} must be a GPU tensor of {dtype}, got {t.dtype} on {t.device}")
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous ({n},) tensor, got {tuple(t.shape)}")
-    return t.data_ptr() or None
+        return 0
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, (n,), dtype, name)
+    return t.data_ptr()
 
 
-def _params(n, default, **vectors):
-    """Pointers of [n] parameter vectors of one type, and that type."""
-    kept = [(k, t) for k, t in vectors.items() if t is not None]
-    dtype = kept[0][1].dtype if kept else default
-    if dtype not in _DT:
-        raise TypeError(f"{kept[0][0]} must be bf16 or float32, got {dtype}")
-    return {k: _vec(t, n, dtype, k) for k, t in vectors.items()}, _DT[dtype]
+def _floats(t, n, name):
+    """Pointer of a contiguous float32 GPU tensor of at least n elements."""
+    if t is None:
+        return 0
+    if t.dtype != _FLOAT or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, (n,), _FLOAT, name)
+    if t.numel() < n:
+        _need(t, n, name)
+    return t.data_ptr()
 
 
-def _gate(gate, rows, cols, name="gate"):
+def _param_type(*vectors):
+    """The one type of a call's parameters, from the first that is given."""
+    for t in vectors:
+        if t is not None:
+            if t.dtype not in _DT:
+                raise TypeError(f"parameters must be bf16 or float32, got {t.dtype}")
+            return t.dtype
+    return _FLOAT
+
+
+def _gate(gate, shape, ptype, name="gate"):
     """(kind, pointer, row stride) of a gate: [cols], [rows, 1] or [rows, cols]."""
+    rows, cols = shape
     if gate is None:
-        return GATE_NONE, None, cols
+        return GATE_NONE, 0, cols
     if gate.dim() == 1:
-        return GATE_CHANNEL, None, cols   # a parameter: its pointer comes with the others
-    if gate.shape == (rows, 1) and (cols != 1 or gate.dtype == torch.float32):
-        if gate.dtype != torch.float32 or not gate.is_cuda or not gate.is_contiguous():
-            raise TypeError(f"a per-token {name} must be a contiguous float32 GPU tensor")
-        return GATE_TOKEN, gate.data_ptr() or None, cols
-    return (GATE_FULL, *_rows(gate, torch.Size((rows, cols)), _BF16, name))
+        return GATE_CHANNEL, _vec(gate, cols, ptype, name), cols
+    if gate.dtype == _FLOAT:
+        if gate.shape != (rows, 1) or not gate.is_cuda or not gate.is_contiguous():
+            _refuse(gate, (rows, 1), _FLOAT, f"a float32 (per-token) {name}")
+        return GATE_TOKEN, gate.data_ptr(), cols
+    return (GATE_FULL, *_mat(gate, shape, _BFLOAT, name))
 
 
-def _workspace(ws, n, like, stream):
-    """(pointer, bytes) of the caller's workspace, or of one from torch's
-    allocator (on the current stream only, whose order keeps it alive)."""
+def _workspace(ws, need, like, stream):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one from
+    torch's allocator (on the current stream only, whose order keeps it)."""
     if ws is None:
         if stream is not None:
             raise ValueError("a call on an explicit stream needs a workspace")
-        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+        ws = torch.empty(need(), dtype=torch.uint8, device=like.device)
     elif not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
-    return ws, ws.data_ptr() or None, ws.numel() * ws.element_size()
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _two_dim(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+    if t.dtype not in _DT:
+        raise TypeError(f"{name} must be bf16 or float32, got {t.dtype}")
+    return t.shape
 
 
 def fp8_block_norm(x, z=None, h=None, y=None, kind=NORM_RMS, eps=1e-6, w_pre=None, b_pre=None,
@@ -518,32 +575,22 @@ def fp8_block_norm(x, z=None, h=None, y=None, kind=NORM_RMS, eps=1e-6, w_pre=Non
     and a per-channel gate [cols] share one type; a gate [rows, 1] is float32, a
     gate [rows, cols] bf16.  stats_z / stats_h [rows, 2] float32 receive (mean,
     1 / deviation) for fp8_block_norm_bwd."""
-    if x.dim() != 2:
-        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
-    shape = x.shape
+    shape = _two_dim(x, "x")
     rows, cols = shape
-    xp, ldx = _rows(x, shape, _ANY, "x")
-    zp, ldz = _rows(z, shape, _BF16, "z")
-    hp, ldh = _rows(h, shape, (x.dtype,), "h")
-    yp, ldy = _rows(y, shape, _BF16, "y")
-    y8p, ldy8 = _rows(y8, shape, _U8, "y8")
-    gk, gp, ldg = _gate(gate, rows, cols)
-    v, pt = _params(cols, torch.float32, w_pre=w_pre, b_pre=b_pre, w_post=w_post, b_post=b_post,
-                    gate=gate if gk == GATE_CHANNEL else None)
-    if y8 is not None:
-        if y8_scaling == SCALE_TENSOR:
-            _need(y8_scale, 1, "y8_scale")
-            _need(y8_amax, 1, "y8_amax")
-        else:
-            _need(y8_scale_inv, rows if y8_scaling == SCALE_ROW else (cols + 127) // 128 * rows, "y8_scale_inv")
-    _need(stats_z, 2 * rows, "stats_z")
-    _need(stats_h, 2 * rows, "stats_h")
-    a = NormArgs(rows, cols, kind, _DT[x.dtype], pt, eps, res_scale, branch_scale, xp, ldx, zp, ldz,
-                 v["w_post"], v["b_post"], v["w_pre"], v["b_pre"], v["gate"] if gk == GATE_CHANNEL else gp, ldg, gk,
-                 gate_act, hp, ldh, _ptr(stats_z, _F32, "stats_z"), _ptr(stats_h, _F32, "stats_h"), yp, ldy,
-                 y8p, ldy8, y8_fmt, y8_scaling, _ptr(y8_scale, _F32, "y8_scale"),
-                 _ptr(y8_scale_inv, _F32, "y8_scale_inv"), _ptr(y8_amax, _F32, "y8_amax"))
-    _check("fp8_block_norm", _L.fp8_block_norm(C.byref(a), _stream(stream)))
+    st = x.dtype
+    pt = _param_type(w_pre, w_post, b_pre, b_post, gate if gate is not None and gate.dim() == 1 else None)
+    gk, gp, ldg = _gate(gate, shape, pt)
+    nsi = 0 if y8_scaling == SCALE_TENSOR else rows if y8_scaling == SCALE_ROW else (cols + 127) // 128 * rows
+    a = _pack_norm(rows, cols, kind, _DT[st], _DT[pt], eps, res_scale, branch_scale, *_mat(x, shape, st, "x"),
+                   *_mat(z, shape, _BFLOAT, "z"), _vec(w_post, cols, pt, "w_post"), _vec(b_post, cols, pt, "b_post"),
+                   _vec(w_pre, cols, pt, "w_pre"), _vec(b_pre, cols, pt, "b_pre"), gp, ldg, gk, gate_act,
+                   *_mat(h, shape, st, "h"), _floats(stats_z, 2 * rows, "stats_z"),
+                   _floats(stats_h, 2 * rows, "stats_h"), *_mat(y, shape, _BFLOAT, "y"), *_codes(y8, shape, "y8"),
+                   y8_fmt, y8_scaling, _floats(y8_scale, 1, "y8_scale"), _floats(y8_scale_inv, nsi, "y8_scale_inv"),
+                   _floats(y8_amax, 1, "y8_amax"))
+    status = _L.fp8_block_norm(a, _stream(stream))
+    if status:
+        _check("fp8_block_norm", status)
 
 
 def fp8_block_norm_bwd_workspace(rows, cols) -> int:
@@ -558,44 +605,45 @@ def fp8_block_norm_bwd(h, dx, dy=None, dh=None, z=None, dz=None, kind=NORM_RMS, 
     """Gradients of fp8_block_norm: of x (dx), z (dz), the weights, biases and
     the gate, from dy (of y; None: y was not made) and dh (what reaches h from
     above; None: nothing).  h, z and the statistics are the forward call's (h:
-    x where there was no z).  Every output but dx may be left out; dx may be dh
-    and dz may be dy."""
-    if h.dim() != 2:
-        raise ValueError(f"h must be 2-D, got {tuple(h.shape)}")
-    shape = h.shape
+    x where there was no z).  Every output may be left out (dx too: None); dx
+    may be dh and dz may be dy."""
+    shape = _two_dim(h, "h")
     rows, cols = shape
-    hp, ldh = _rows(h, shape, _ANY, "h")
-    dxp, lddx = _rows(dx, shape, (h.dtype,), "dx")
-    dyp, lddy = _rows(dy, shape, _BF16, "dy")
-    dhp, lddh = _rows(dh, shape, (h.dtype,), "dh")
-    zp, ldz = _rows(z, shape, _BF16, "z")
-    dzp, lddz = _rows(dz, shape, _BF16, "dz")
-    gk, gp, ldg = _gate(gate, rows, cols)
-    dgp, lddg = None, cols
-    channel = gk == GATE_CHANNEL
+    st = h.dtype
+    pt = _param_type(w_pre, w_post, dw_pre, dw_post, b_post, db_pre, db_post,
+                     gate if gate is not None and gate.dim() == 1 else None)
+    gk, gp, ldg = _gate(gate, shape, pt)
+    dgp, lddg = 0, cols
     if dgate is not None:
         if gate is None or dgate.shape != gate.shape or dgate.dtype != gate.dtype:
             raise ValueError("dgate must have the gate's shape and type")
-        if not channel:
-            _, dgp, lddg = _gate(dgate, rows, cols, "dgate")
-    v, pt = _params(cols, torch.float32, w_pre=w_pre, w_post=w_post, b_post=b_post,
-                    gate=gate if channel else None, dgate=dgate if channel else None,
-                    dw_pre=dw_pre, db_pre=db_pre, dw_post=dw_post, db_post=db_post)
-    _need(stats_z, 2 * rows, "stats_z")
-    _need(stats_h, 2 * rows, "stats_h")
-    ws, wp, wn = _workspace(workspace, _L.fp8_block_norm_bwd_workspace(rows, cols) if workspace is None else 0, h,
-                            stream)
-    a = NormBwdArgs(rows, cols, kind, _DT[h.dtype], pt, res_scale, branch_scale, dyp, lddy, dhp, lddh, hp, ldh,
-                    _ptr(stats_h, _F32, "stats_h"), zp, ldz, _ptr(stats_z, _F32, "stats_z"), v["w_post"],
-                    v["b_post"], v["w_pre"], v["gate"] if channel else gp, ldg, gk, gate_act, dxp, lddx, dzp, lddz,
-                    v["dgate"] if channel else dgp, lddg, v["dw_pre"], v["db_pre"], v["dw_post"], v["db_post"],
-                    wp, wn)
-    _check("fp8_block_norm_bwd", _L.fp8_block_norm_bwd(C.byref(a), _stream(stream)))
+        _, dgp, lddg = _gate(dgate, shape, pt, "dgate")
+    ws, wp, wn = _workspace(workspace, lambda: _L.fp8_block_norm_bwd_workspace(rows, cols), h, stream)
+    a = _pack_norm_bwd(rows, cols, kind, _DT[st], _DT[pt], res_scale, branch_scale, *_mat(dy, shape, _BFLOAT, "dy"),
+                       *_mat(dh, shape, st, "dh"), *_mat(h, shape, st, "h"), _floats(stats_h, 2 * rows, "stats_h"),
+                       *_mat(z, shape, _BFLOAT, "z"), _floats(stats_z, 2 * rows, "stats_z"),
+                       _vec(w_post, cols, pt, "w_post"), _vec(b_post, cols, pt, "b_post"),
+                       _vec(w_pre, cols, pt, "w_pre"), gp, ldg, gk, gate_act, *_mat(dx, shape, st, "dx"),
+                       *_mat(dz, shape, _BFLOAT, "dz"), dgp, lddg, _vec(dw_pre, cols, pt, "dw_pre"),
+                       _vec(db_pre, cols, pt, "db_pre"), _vec(dw_post, cols, pt, "dw_post"),
+                       _vec(db_post, cols, pt, "db_post"), wp, wn)
+    status = _L.fp8_block_norm_bwd(a, _stream(stream))
+    if status:
+        _check("fp8_block_norm_bwd", status)
 
 
 def fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling) -> int:
     """Bytes of workspace that fp8_scaled_gemm_ep needs."""
     return _L.fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling)
+
+
+def _scales(t, scaling, rows, nkb, name):
+    n = (1 if scaling == SCALE_TENSOR else rows if scaling == SCALE_ROW else
+         nkb * (rows if scaling in (SCALE_1x128, SCALE_1x128_POW2) else (rows + 127) // 128))
+    return _floats(t, n if nkb > 0 else 0, name)
+
+
+_OUT = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
 
 
 def fp8_scaled_gemm_ep(A, a_fmt, a_scaling, a_scale_inv, B, b_fmt, b_scaling, b_scale_inv, D, bias=None,
@@ -610,36 +658,36 @@ def fp8_scaled_gemm_ep(A, a_fmt, a_scaling, a_scale_inv, B, b_fmt, b_scaling, b_
     rows; bias and dbias are [N] bf16 or float32."""
     M, K = A.shape
     N = B.shape[0]
-    ap, lda = _rows(A, A.shape, _U8, "A")
-    bp, ldb = _rows(B, torch.Size((N, K)), _U8, "B")
     mn = torch.Size((M, N))
-    if D.dtype in _U8:
+    dt = D.dtype
+    if dt in _U8:
         if d_fmt not in (E4M3, E5M2):
             raise ValueError("an FP8 output needs d_fmt (E4M3 or E5M2)")
         d_dtype = OUT_E4M3 if d_fmt == E4M3 else OUT_E5M2
+    elif dt in _OUT:
+        d_dtype = _OUT[dt]
     else:
-        d_dtype = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}[D.dtype]
-    dp, ldd = _rows(D, mn, (D.dtype,), "D")
-    tp, ldt = _rows(D_t, torch.Size((N, M)), _U8, "D_t")
-    xp, ldaux = _rows(aux, mn, _BF16, "aux")
-    rp, ldres = _rows(residual, mn, _ANY, "residual")
-    v, pt = _params(N, torch.float32, bias=bias, dbias=dbias)
-    nkb = (K + 127) // 128
-    for s, scaling, rows, name in ((a_scale_inv, a_scaling, M, "a_scale_inv"), (b_scale_inv, b_scaling, N, "b_scale_inv")):
-        if M > 0 and N > 0 and K > 0:
-            _need(s, 1 if scaling == SCALE_TENSOR else rows if scaling == SCALE_ROW else
-                  nkb * (rows if scaling in (SCALE_1x128, SCALE_1x128_POW2) else (rows + 127) // 128), name)
-    _need(d_amax, 1, "d_amax")
-    _need(d_scale, 1, "d_scale")
-    ws, wp, wn = _workspace(workspace, _L.fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling)
-                            if workspace is None else 0, A, stream)
-    g = GemmArgs(M, N, K, lda, ldb, ldd, ap, a_fmt, a_scaling, _ptr(a_scale_inv, _F32, "a_scale_inv"),
-                 bp, b_fmt, b_scaling, _ptr(b_scale_inv, _F32, "b_scale_inv"), dp, d_dtype,
-                 _ptr(d_amax, _F32, "d_amax"), 0, _ptr(d_scale, _F32, "d_scale"), tp, ldt,
-                 1 if amax_accumulate else 0)
-    e = EpilogueArgs(1 if backward else 0, act, pt, v["bias"], rp, ldres,
-                     DT_BF16 if residual is None else _DT[residual.dtype], res_scale, xp, ldaux, v["dbias"], wp, wn)
-    _check("fp8_scaled_gemm_ep", _L.fp8_scaled_gemm_ep(C.byref(g), C.byref(e), _stream(stream)))
+        raise TypeError(f"D has dtype {dt}, expected bf16, float32 or FP8 codes")
+    pt = _param_type(bias, dbias)
+    rt = _BFLOAT if residual is None else residual.dtype
+    if rt not in _DT:
+        raise TypeError(f"residual must be bf16 or float32, got {rt}")
+    nkb = (K + 127) // 128 if M > 0 and N > 0 else 0
+    ap, lda = _codes(A, A.shape, "A")
+    bp, ldb = _codes(B, torch.Size((N, K)), "B")
+    dp, ldd = _mat(D, mn, dt, "D")
+    tp, ldt = _codes(D_t, torch.Size((N, M)), "D_t") if D_t is not None else (0, M)
+    ws, wp, wn = _workspace(workspace, lambda: _L.fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling), A,
+                            stream)
+    g = _pack_gemm(M, N, K, lda, ldb, ldd, ap, a_fmt, a_scaling, _scales(a_scale_inv, a_scaling, M, nkb, "a_scale_inv"),
+                   bp, b_fmt, b_scaling, _scales(b_scale_inv, b_scaling, N, nkb, "b_scale_inv"), dp, d_dtype,
+                   _floats(d_amax, 1, "d_amax"), 0, _floats(d_scale, 1, "d_scale"), tp, ldt,
+                   1 if amax_accumulate else 0)
+    e = _pack_ep(1 if backward else 0, act, _DT[pt], _vec(bias, N, pt, "bias"), *_mat(residual, mn, rt, "residual"),
+                 _DT[rt], res_scale, *_mat(aux, mn, _BFLOAT, "aux"), _vec(dbias, N, pt, "dbias"), wp, wn)
+    status = _L.fp8_scaled_gemm_ep(g, e, _stream(stream))
+    if status:
+        _check("fp8_scaled_gemm_ep", status)
 
 
 def fp8_rope_freqs(freqs, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, trained=8192.0, low=1.0, high=32.0,
@@ -652,13 +700,14 @@ def fp8_rope_freqs(freqs, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, trained=
                              low, high, _stream(stream)))
 
 
-def _heads(t, tokens, dim, dtype, name):
-    if not t.is_cuda or t.dtype != dtype:
-        raise TypeError(f"{name} must be a GPU tensor of {dtype}, got {t.dtype} on {t.device}")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim or (dim > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be [{tokens}][heads][{dim}] with unit stride inside a head, got "
-                         f"{tuple(t.shape)}, strides {t.stride()}")
-    return t.shape[1], t.data_ptr() or None, t.stride(0), t.stride(1)
+def _heads(t, shape, dtype, name):
+    """(pointer, token stride, head stride) of [tokens][heads][dim] heads."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda:
+        _refuse(t, shape, dtype, name)
+    ts, hs, one = t.stride()
+    if one != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must have unit stride inside a head, got strides {t.stride()}")
+    return t.data_ptr(), ts, hs
 
 
 def fp8_rope(q, freqs, positions=None, k=None, q_out=None, k_out=None, layout=ROPE_HALF, inverse=False,
@@ -669,26 +718,29 @@ def fp8_rope(q, freqs, positions=None, k=None, q_out=None, k_out=None, layout=RO
     QKV tensor; without q_out / k_out they are turned in place.  positions:
     [tokens] int32 or int64 (None: 0, 1, ...).  inverse=True turns back: the
     gradient."""
-    tokens, _, dim = q.shape
-    qh, qp, qs, qhs = _heads(q, tokens, dim, q.dtype if q.dtype in _DT else torch.bfloat16, "q")
-    qo = q if q_out is None else q_out
-    qoh, qop, qos, qohs = _heads(qo, tokens, dim, q.dtype, "q_out")
-    kh, kp, ks, khs, kop, kos, kohs = 0, None, 0, 0, None, 0, 0
+    shape, dt = q.shape, q.dtype
+    if dt not in _DT:
+        raise TypeError(f"q must be bf16 or float32, got {dt}")
+    if len(shape) != 3:
+        raise ValueError(f"q must be [tokens][heads][dim], got {tuple(shape)}")
+    tokens, qh, dim = shape
+    qv = _heads(q, shape, dt, "q")
+    qo = qv if q_out is None else _heads(q_out, shape, dt, "q_out")
+    kh, kv, ko = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
-        kh, kp, ks, khs = _heads(k, tokens, dim, q.dtype, "k")
-        koh, kop, kos, kohs = _heads(k if k_out is None else k_out, tokens, dim, q.dtype, "k_out")
-        if koh != kh:
-            raise ValueError("k_out must have k's heads")
-    if qoh != qh:
-        raise ValueError("q_out must have q's heads")
-    pp, wide = None, 0
+        kshape = k.shape
+        if len(kshape) != 3 or kshape[0] != tokens or kshape[2] != dim:
+            raise ValueError(f"k must be [{tokens}][heads][{dim}], got {tuple(kshape)}")
+        kh = kshape[1]
+        kv = _heads(k, kshape, dt, "k")
+        ko = kv if k_out is None else _heads(k_out, kshape, dt, "k_out")
+    pp, wide = 0, 0
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-        if positions.shape != (tokens,):
-            raise ValueError(f"positions must be ({tokens},), got {tuple(positions.shape)}")
-        pp, wide = _ptr(positions, None, "positions"), 1 if positions.dtype == torch.int64 else 0
-    a = RopeArgs(tokens, qh, kh, dim, freqs.numel(), _DT[q.dtype], layout, 1 if inverse else 0, scale,
-                 _ptr(freqs, (torch.float64,), "freqs"), pp, wide, offset, qp, qs, qhs, kp, ks, khs,
-                 qop, qos, qohs, kop, kos, kohs)
-    _check("fp8_rope", _L.fp8_rope(C.byref(a), _stream(stream)))
+        wide = 1 if positions.dtype == torch.int64 else 0
+        pp = _vec(positions, tokens, torch.int64 if wide else torch.int32, "positions")
+    pairs = freqs.numel()
+    a = _pack_rope(tokens, qh, kh, dim, pairs, _DT[dt], layout, 1 if inverse else 0, scale,
+                   _vec(freqs, pairs, torch.float64, "freqs"), pp, wide, offset, *qv, *kv, *qo, *ko)
+    status = _L.fp8_rope(a, _stream(stream))
+    if status:
+        _check("fp8_rope", status)
