@@ -150,6 +150,7 @@ fp8_status fp8_scaled_gemm_ep(const fp8_gemm_args* gemm, const fp8_epilogue_args
   if (!dtype_ok(ep->param_dtype) || !dtype_ok(ep->residual_dtype)) return FP8_ERR_ARG;
   if (ep->backward ? (ep->bias != nullptr || ep->residual != nullptr) : ep->dbias != nullptr) return FP8_ERR_ARG;
   if (a->accumulate) return FP8_ERR_UNSUPPORTED;
+  if (p.d_fp8 && ep->residual != nullptr && ep->residual_dtype == FP8_DT_F32) return FP8_ERR_UNSUPPORTED;
   if (a->M > 0 && a->N > 0) {
     if (ep->backward && ep->act != FP8_ACT_NONE && ep->aux == nullptr) return FP8_ERR_NULL;
     if (ep->aux != nullptr && ep->ldaux < a->N) return FP8_ERR_SHAPE;

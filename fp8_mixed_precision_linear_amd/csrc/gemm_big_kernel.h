@@ -426,8 +426,11 @@ __device__ __forceinline__ void workgroup_amax(float* d_amax, uint32_t amax_bits
 // SA_ROWS: A has 1x128 scales (one per row and K block), else one per wave;
 // SB_COL : B has 1x128 scales (one per column and K block), else one per wave;
 // MX     : always false here.
-template <int AF, int BF, bool BLOCK, bool SA_ROWS, bool SB_COL, bool MX, bool OUT8>
-__global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m, int tiles_n) {
+// EP     : the linear's epilogue (gemm_ep.h) in place of the plain one, its
+//          arguments in `ep` (NoEpilogue: none).
+struct NoEpilogue {};
+template <int AF, int BF, bool BLOCK, bool SA_ROWS, bool SB_COL, bool MX, bool OUT8, typename EP = NoEpilogue>
+__global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   static_assert(BLOCK && !MX, "per-tensor, per-row and power-of-two scales run on k_gemm_w4");
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE];
   __shared__ float su_tab[NWAVES][MAX_KB];
@@ -644,6 +647,12 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
   // dequantised value of accumulator entry (i, j, q): the promoted
   // accumulators carry their scales
   auto deq = [&](int, int, int, float a) -> float { return a; };
+  if constexpr (!std::is_same_v<EP, NoEpilogue>) {
+    __syncthreads();   // every wavefront is done reading both stages
+    ep.template finish<OUT8, TI, TJ, NWAVES>(p, acc, deq, m0 + wm * WTM, n0 + wn * WTN, tm * 2 + wm, lane, wave,
+                                             &lds[0][0] + wave * 16384);
+    return;
+  }
   const int esz = OUT8 ? 1 : (p.d_f32 ? 4 : 2);
   const bool staged = (m0 + BM <= M) && (n0 + BN <= N) && ((p.ldd * esz) % 16 == 0) &&
                       ((reinterpret_cast<uintptr_t>(p.D) & 15u) == 0) &&
@@ -669,7 +678,7 @@ hipError_t launch_one(const GemmParams& p, hipStream_t s) {
   auto kern = k_gemm_big<AF, BF, BLOCK, SA_ROWS, SB_COL, MX, OUT8>;
   const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
   hipLaunchKernelGGL(kern, dim3((unsigned)(tiles_m * tiles_n)), dim3(THREADS), 0, s, p, tiles_m,
-                     tiles_n);
+                     tiles_n, NoEpilogue{});
   return hipGetLastError();
 }
 

@@ -26,41 +26,171 @@ namespace {
 typedef float v4f_ep __attribute__((ext_vector_type(4)));
 struct __attribute__((packed, aligned(1))) Pk16a1 { uint32_t v[4]; };
 
-template <int ACT>
-__device__ __forceinline__ void act8(float (&v)[8]) {
+// A uniform run-time choice per eight values: one scalar branch.  The tanh form of
+// GELU and SiLU are the same code with other factors.
+template <bool SLOPE>
+__device__ __forceinline__ void activate(int act, float (&v)[8], const float (&u)[8]) {
+  if (act == 0) return;
+  if (act >= 3) {
+    const SigmoidForm f(act);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = act_value<ACT>(v[k]);
-}
-template <int ACT>
-__device__ __forceinline__ void slope8(float (&v)[8], const float (&u)[8]) {
+    for (int k = 0; k < 8; ++k) v[k] = SLOPE ? v[k] * f.slope(u[k]) : f.value(u[k]);
+  } else if (act == 2) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] *= act_slope<ACT>(u[k]);
-}
-// A uniform run-time choice per eight values: one scalar branch.
-__device__ __forceinline__ void apply_act(int act, float (&v)[8]) {
-  switch (act) {
-    case 1: act8<1>(v); break;
-    case 2: act8<2>(v); break;
-    case 3: act8<3>(v); break;
-    case 4: act8<4>(v); break;
-    default: break;
-  }
-}
-__device__ __forceinline__ void apply_slope(int act, float (&v)[8], const float (&u)[8]) {
-  switch (act) {
-    case 1: slope8<1>(v, u); break;
-    case 2: slope8<2>(v, u); break;
-    case 3: slope8<3>(v, u); break;
-    case 4: slope8<4>(v, u); break;
-    default: break;
+    for (int k = 0; k < 8; ++k) v[k] = SLOPE ? v[k] * gelu_erf<true>(u[k]) : gelu_erf<false>(u[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = SLOPE ? (u[k] > 0.0f ? v[k] : 0.0f * v[k]) : (u[k] <= 0.0f ? 0.0f : u[k]);
   }
 }
 
+// Eight values of a row of bf16 or binary32, as they lie in memory (see Raw8 in
+// op_device.h); n: how many there are.
+template <bool FAST, int W>
+__device__ __forceinline__ void load_packed(const void* p, int f32, int n, uint32_t (&w)[W]) {
+  if (n <= 0) return;
+  if constexpr (FAST) {
+    const Pk16a4 a = *reinterpret_cast<const Pk16a4*>(p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = a.v[k];
+    if constexpr (W == 8) {
+      if (f32) {
+        const Pk16a4 b = *(reinterpret_cast<const Pk16a4*>(p) + 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k + 4] = b.v[k];
+      }
+    }
+    return;
+  } else {
+  if constexpr (W == 8) {
+    if (f32) {
+      const float* q = reinterpret_cast<const float*>(p);
+      if (n >= 8) {
+        const Pk16a4 a = *reinterpret_cast<const Pk16a4*>(q);
+        const Pk16a4 b = *reinterpret_cast<const Pk16a4*>(q + 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          w[k] = a.v[k];
+          w[k + 4] = b.v[k];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = k < n ? __float_as_uint(q[k]) : 0u;
+      }
+      return;
+    }
+  }
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+  uint32_t d[5] = {0u, 0u, 0u, 0u, 0u};
+  if (n >= 8) {
+    load_dwords(q, d);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (k < n) d[k >> 1] |= (uint32_t)q[k] << (16 * (k & 1));
+    if (odd_of(p)) {
+#pragma unroll
+      for (int k = 4; k >= 1; --k) d[k] = __builtin_amdgcn_alignbyte(d[k], d[k - 1], 2);
+      d[0] <<= 16;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 5; ++k) w[k] = d[k];
+  }
+}
+
+// Eight bf16 or binary32 values, or eight codes, to p, by SEG neighbouring lanes
+// per row (see store_row); n: how many are written.
+template <int SEG, bool FAST>
+__device__ __forceinline__ void put8(void* p, int f32, int n, const float (&v)[8]) {
+  if (f32) {
+    if (!FAST) store8(p, 1, 0, n, v);
+    else if (n > 0) store8(p, 1, 0, 8, v);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+  if constexpr (FAST) {
+    if (n > 0) {
+      Pk16a4 a;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a.v[k] = w[k];
+      *reinterpret_cast<Pk16a4*>(p) = a;
+    }
+    return;
+  }
+  store_row<4, SEG>(reinterpret_cast<uint8_t*>(p), w, n >= 8);
+  if (n > 0 && n < 8) {
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (k < n) reinterpret_cast<uint16_t*>(p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+  }
+}
+template <int SEG, bool FAST>
+__device__ __forceinline__ void put8_codes(uint8_t* p, int n, uint32_t lo, uint32_t hi) {
+  if constexpr (FAST) {
+    struct __attribute__((packed, aligned(4))) Two { uint32_t a, b; };
+    if (n > 0) *reinterpret_cast<Two*>(p) = Two{lo, hi};
+    return;
+  }
+  const uint32_t w[2] = {lo, hi};
+  store_row<2, SEG>(p, w, n >= 8);
+  if (n > 0 && n < 8) {
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (k < n) p[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+  }
+}
+
+// Eight codes; a NaN (rare) is patched in place, without a call, which would
+// spill the caller's accumulators.
+template <int FMT>
+__device__ __forceinline__ void encode8(const float (&x)[8], uint32_t& lo, uint32_t& hi) {
+  int a, b;
+  if constexpr (FMT == 0) {
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(sat<0>(x[0]), sat<0>(x[1]), 0, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(sat<0>(x[2]), sat<0>(x[3]), a, true);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(sat<0>(x[4]), sat<0>(x[5]), 0, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(sat<0>(x[6]), sat<0>(x[7]), b, true);
+  } else {
+    a = __builtin_amdgcn_cvt_pk_bf8_f32(sat<1>(x[0]), sat<1>(x[1]), 0, false);
+    a = __builtin_amdgcn_cvt_pk_bf8_f32(sat<1>(x[2]), sat<1>(x[3]), a, true);
+    b = __builtin_amdgcn_cvt_pk_bf8_f32(sat<1>(x[4]), sat<1>(x[5]), 0, false);
+    b = __builtin_amdgcn_cvt_pk_bf8_f32(sat<1>(x[6]), sat<1>(x[7]), b, true);
+  }
+  lo = (uint32_t)a;
+  hi = (uint32_t)b;
+  bool nan = false;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) nan |= __builtin_isunordered(x[k], x[k + 1]);
+  if (__builtin_expect(nan, 0)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t code = 0x7Fu | ((__float_as_uint(x[k]) >> 24) & 0x80u), w = k < 4 ? lo : hi;
+      const int s = 8 * (k & 3);
+      const uint32_t q = x[k] == x[k] ? w : ((w & ~(0xFFu << s)) | (code << s));
+      if (k < 4) lo = q;
+      else hi = q;
+    }
+  }
+}
+
+// FAST: whole vectors only (N a multiple of 8) that start on a dword in every row;
+// the others' accesses of single elements are a third of the code, and in the
+// large kernels, whose epilogue is unrolled over 8 strips, more than the
+// instruction cache holds.
+// Directions of an epilogue: fixed at compile time in the large kernels (half the
+// code), by EpParams::backward in the others.
+enum : int { EP_FWD = 0, EP_BWD = 1, EP_ANY = 2 };
+
 // One wavefront's columns n0 .. n0 + WTN - 1, lane's columns c .. c + 7.
-template <int WTN, bool OUT8>
+template <int WTN, bool OUT8, int DIR, bool FAST>
 struct EpWave {
   static constexpr int LPR = WTN / 8;        // lanes per row
   static constexpr int RPL = WTN / 32;       // rows per lane and strip of 16
+  static constexpr int CH = WTN / 4;         // 16-byte chunks of a strip's row
+  static constexpr int SW = OUT8 ? (FAST ? 4 : 5) : 8;   // words of eight values of src in flight
   const GemmParams& p;
   const EpParams& e;
   int lane, cq, rg, nv;
@@ -68,6 +198,11 @@ struct EpWave {
   float bias[8], db[8];
   uint32_t amax = 0;
   float so;
+  const char* src;      // what is read beside the product: pre-activation (backward) or residual
+  int64_t src_ld;       // bytes per row
+  int src_f32;
+
+  __device__ __forceinline__ bool backward() const { return DIR == EP_ANY ? e.backward != 0 : DIR == EP_BWD; }
 
   __device__ __forceinline__ EpWave(const GemmParams& p_, const EpParams& e_, int64_t n0, int lane_)
       : p(p_), e(e_), lane(lane_), cq(lane_ % LPR), rg(lane_ / LPR), c(n0 + 8 * (lane_ % LPR)) {
@@ -75,122 +210,169 @@ struct EpWave {
     nv = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
 #pragma unroll
     for (int k = 0; k < 8; ++k) { bias[k] = 0.0f; db[k] = 0.0f; }
-    if (e.bias) load8(e.bias, e.bias_f32, c, nv, bias);
+    if (!backward() && e.bias) load8(e.bias, e.bias_f32, c, nv, bias);
     so = OUT8 ? p.d_scale[0] : 1.0f;
+    src_f32 = backward() || OUT8 ? 0 : e.res_f32;
+    const int es = src_f32 ? 4 : 2;
+    src = reinterpret_cast<const char*>(backward() ? (e.act ? e.aux : nullptr) : e.residual);
+    src_ld = (backward() ? e.ldaux : e.ldres) * es;
+    if (src) src += c * es;
   }
 
-  // What the strip of rows m0 .. m0 + 15 reads beside the product: the
-  // pre-activation (backward) or the residual.
-  __device__ __forceinline__ void fetch(int64_t m0, float (&o)[RPL][8]) {
-    const void* src = e.backward ? (e.act ? e.aux : nullptr) : e.residual;
+  // The strip of rows m0 .. m0 + 15 of src, in flight until stage() puts it into
+  // LDS, where the loop over the rows can index it.
+  __device__ __forceinline__ void fetch(int64_t m0, uint32_t (&o)[RPL][SW]) {
     if (src == nullptr) return;
-    const int f32 = e.backward ? 0 : e.res_f32;
-    const int64_t ld = e.backward ? e.ldaux : e.ldres;
 #pragma unroll
     for (int t = 0; t < RPL; ++t) {
       const int64_t m = m0 + rg * RPL + t;
-      load8(src, f32, m * ld + c, m < p.M ? nv : 0, o[t]);
+      load_packed<FAST>(src + m * src_ld, src_f32, m < p.M ? nv : 0, o[t]);
+    }
+  }
+  // Each lane's own words: 16 bytes per lane and row for bf16, twice that for
+  // binary32.
+  static constexpr int SRC_BYTES = RPL * 64 * 16;
+  __device__ __forceinline__ void stage(int64_t m0, const uint32_t (&o)[RPL][SW], uint8_t* ol) {
+    if (src == nullptr) return;
+    uint4* q = reinterpret_cast<uint4*>(ol) + lane;
+#pragma unroll
+    for (int t = 0; t < RPL; ++t) {
+      if (FAST || src_f32) q[t * 64] = make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
+      if constexpr (!OUT8) {
+        if (src_f32) q[(RPL + t) * 64] = make_uint4(o[t][4], o[t][5], o[t][6], o[t][7]);
+      }
+      if constexpr (!FAST) {
+        if (src_f32) continue;
+        const uint32_t s = odd_of(src + (m0 + rg * RPL + t) * src_ld);
+        q[t * 64] = make_uint4(__builtin_amdgcn_alignbyte(o[t][1], o[t][0], s), __builtin_amdgcn_alignbyte(o[t][2], o[t][1], s),
+                               __builtin_amdgcn_alignbyte(o[t][3], o[t][2], s), __builtin_amdgcn_alignbyte(o[t][4], o[t][3], s));
+      }
     }
   }
 
-  // The strip: v[t] is row m0 + rg RPL + t.  tl: column-major codes of the
-  // wavefront (TS bytes per column, this strip's rows at byte tr), if D_t.
+  // Where the strip's row r keeps columns 4 q .. 4 q + 3.
+  static __device__ __forceinline__ float4* place(uint8_t* wl, int r, int q) {
+    return reinterpret_cast<float4*>(wl + r * (WTN * 4) + ((q ^ (r & (CH - 1))) << 4));
+  }
+
+  // The strip in wl, rows m0 + rg RPL + t for t = 0 .. RPL - 1, one after the
+  // other in a loop that stays one: unrolled over its 4 rows and a wavefront's 8
+  // strips the epilogue was 44000 instructions, several times the instruction
+  // cache.  ol: src's rows (stage); tl: column-major codes of the wavefront (TS
+  // bytes per column, this strip's rows at byte tr), if D_t.
   template <int TS>
-  __device__ __forceinline__ void strip(int64_t m0, float (&v)[RPL][8], const float (&o)[RPL][8], uint8_t* tl,
-                                        int tr) {
-    uint32_t lo[RPL], hi[RPL];
-#pragma unroll
+  __device__ __forceinline__ void rows(int64_t m0, uint8_t* wl, const uint8_t* ol, uint8_t* tl, int tr) {
+    uint32_t turned[8] = {};
+    const int64_t first = m0 + rg * RPL;
+    const int esz = OUT8 ? 1 : (p.d_f32 ? 4 : 2);
+    char* d = reinterpret_cast<char*>(p.D) + (first * p.ldd + c) * esz;
+    char* aux = (!backward() && e.aux)
+                    ? reinterpret_cast<char*>(const_cast<void*>(e.aux)) + (first * e.ldaux + c) * 2 : nullptr;
+    const uint4* q = reinterpret_cast<const uint4*>(ol) + lane;
+    const bool wide = !OUT8 && src != nullptr && src_f32;
+#pragma unroll 1
     for (int t = 0; t < RPL; ++t) {
-      const int64_t m = m0 + rg * RPL + t;
-      const int n = m < p.M ? nv : 0;
-      if (!e.backward) {
+      const float4 w0 = *place(wl, rg * RPL + t, 2 * cq), w1 = *place(wl, rg * RPL + t, 2 * cq + 1);
+      float v[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      const int n = first + t < p.M ? nv : 0;
+      float u[8];
+      if (src) {
+        const uint4 a = q[t * 64];
+        if (wide) {
+          const uint4 b = q[(RPL + t) * 64];
+          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[t][k] += bias[k];
-        if (e.aux) store8(const_cast<void*>(e.aux), 0, m * e.ldaux + c, n, v[t]);
-        apply_act(e.act, v[t]);
-        if (e.residual) {
+          for (int k = 0; k < 8; ++k) u[k] = __uint_as_float(w[k]);
+        } else {
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[t][k] = __builtin_fmaf(e.res_scale, o[t][k], v[t][k]);
+          for (int k = 0; k < 4; ++k) {
+            u[2 * k] = bf16_lo(w[k]);
+            u[2 * k + 1] = bf16_hi(w[k]);
+          }
+        }
+      }
+      if (!backward()) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += bias[k];
+        if (aux) put8<LPR, FAST>(aux, 0, n, v);
+        activate<false>(e.act, v, v);
+        if (src) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(e.res_scale, u[k], v[k]);
         }
       } else {
-        apply_slope(e.act, v[t], o[t]);
+        if (src) activate<true>(e.act, v, u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) db[k] += k < n ? v[t][k] : 0.0f;
+        for (int k = 0; k < 8; ++k) db[k] += (FAST ? n > 0 : k < n) ? v[k] : 0.0f;
       }
       if (p.d_amax) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = max_u32(amax, k < n ? abs_bits(v[t][k]) : 0u);
+        for (int k = 0; k < 8; ++k) amax = max_u32(amax, (FAST ? n > 0 : k < n) ? abs_bits(v[k]) : 0u);
       }
       if constexpr (OUT8) {
-        codes8(p.d_fp8 - 1, v[t], so, lo[t], hi[t]);
-        store8_codes(reinterpret_cast<uint8_t*>(p.D), m * p.ldd + c, n, lo[t], hi[t]);
+        uint32_t lo, hi;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= so;
+        if (p.d_fp8 == 1) encode8<0>(v, lo, hi);
+        else encode8<1>(v, lo, hi);
+        put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
+        if (p.D_t) {   // code k to the top of column k's word, the rows before down a byte
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            turned[k] = __builtin_amdgcn_perm(k < 4 ? lo : hi, turned[k], 0x00030201u | ((uint32_t)(4 + (k & 3)) << 24));
+        }
       } else {
-        store8(p.D, p.d_f32, m * p.ldd + c, n, v[t]);
+        put8<LPR, FAST>(d, p.d_f32, n, v);
       }
+      d += p.ldd * esz;
+      if (aux) aux += e.ldaux * 2;
     }
     if constexpr (OUT8) {
       if (p.D_t) {
         uint8_t* dst = tl + (8 * cq) * TS + tr + rg * RPL;
-        if constexpr (RPL == 4) {
-          uint32_t w[8];
-          transpose4x4(lo[0], lo[1], lo[2], lo[3], w[0], w[1], w[2], w[3]);
-          transpose4x4(hi[0], hi[1], hi[2], hi[3], w[4], w[5], w[6], w[7]);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint32_t*>(dst + k * TS) = w[k];
-        } else {
-          static_assert(RPL == 2, "two or four rows per lane");
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t a = (k < 4 ? lo[0] : hi[0]) >> (8 * (k & 3)), b = (k < 4 ? lo[1] : hi[1]) >> (8 * (k & 3));
-            *reinterpret_cast<uint16_t*>(dst + k * TS) = (uint16_t)((a & 0xFFu) | ((b & 0xFFu) << 8));
+        for (int k = 0; k < 8; ++k) {
+          if constexpr (RPL == 4) {
+            *reinterpret_cast<uint32_t*>(dst + k * TS) = turned[k];
+          } else {
+            static_assert(RPL == 2, "two or four rows per lane");
+            *reinterpret_cast<uint16_t*>(dst + k * TS) = (uint16_t)(turned[k] >> 16);
           }
         }
       }
     }
+    asm volatile("" ::: "memory");   // LDS is written and read as different types
   }
 
+  // LDS of a wavefront of TI strips: the strip (64 WTN bytes), src's rows, then
+  // (OUT8) the column-major codes.  (An FP8
+  // output takes a bf16 residual only, so its src words are half as many.)
+  static constexpr int strip_at = 0, src_at = 64 * WTN;
+  static constexpr int codes_at = src_at + (OUT8 ? 1 : 2) * SRC_BYTES;
+  static constexpr int bytes(int TI) { return codes_at + (OUT8 ? WTN * (16 * TI + 16) : 0); }
+
   // Accumulators to strips.  acc[i][j] of lane (g, l16): row r0 + 16 i + l16,
-  // columns n0 + 16 j + 4 g .. + 3.  wl: 64 WTN bytes for the strip, then
-  // (D_t) WTN columns of 16 TI + 16 bytes, wavefront-private.
+  // columns n0 + 16 j + 4 g .. + 3.  wl: bytes(TI) of LDS, wavefront-private.
   template <int TI, int TJ, typename Deq>
   __device__ __forceinline__ void tile(const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t n0, uint8_t* wl) {
     static_assert(16 * TJ == WTN, "the wavefront's columns");
-    constexpr int TS = 16 * TI + 16, CH = WTN / 4;
+    constexpr int TS = 16 * TI + 16;
     const int g = lane >> 4, l16 = lane & 15;
-    uint8_t* tl = wl + 64 * WTN;
-    float o[2][RPL][8];
-    fetch(r0, o[0]);
+    uint32_t o[RPL][SW];
+    fetch(r0, o);
     ep_for<0, TI>([&](auto itag) {
       constexpr int i = decltype(itag)::value;
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        float4 w;
-        w.x = deq(i, j, 0, acc[i][j][0]);
-        w.y = deq(i, j, 1, acc[i][j][1]);
-        w.z = deq(i, j, 2, acc[i][j][2]);
-        w.w = deq(i, j, 3, acc[i][j][3]);
-        *reinterpret_cast<float4*>(wl + l16 * (WTN * 4) + (((4 * j + g) ^ (l16 & (CH - 1))) << 4)) = w;
-      }
-      if constexpr (i + 1 < TI) fetch(r0 + 16 * (i + 1), o[(i + 1) & 1]);
-      float v[RPL][8];
-#pragma unroll
-      for (int t = 0; t < RPL; ++t) {
-        const int r = rg * RPL + t;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 w =
-              *reinterpret_cast<const float4*>(wl + r * (WTN * 4) + (((2 * cq + h) ^ (r & (CH - 1))) << 4));
-          v[t][4 * h] = w.x;
-          v[t][4 * h + 1] = w.y;
-          v[t][4 * h + 2] = w.z;
-          v[t][4 * h + 3] = w.w;
-        }
-      }
-      strip<TS>(r0 + 16 * i, v, o[i & 1], tl, 16 * i);
+      for (int j = 0; j < TJ; ++j)
+        *place(wl, l16, 4 * j + g) = make_float4(deq(i, j, 0, acc[i][j][0]), deq(i, j, 1, acc[i][j][1]),
+                                                 deq(i, j, 2, acc[i][j][2]), deq(i, j, 3, acc[i][j][3]));
+      stage(r0 + 16 * i, o, wl + src_at);
+      if constexpr (i + 1 < TI) fetch(r0 + 16 * (i + 1), o);
+      rows<TS>(r0 + 16 * i, wl, wl + src_at, wl + codes_at, 16 * i);
     });
     if constexpr (OUT8) {
-      asm volatile("" ::: "memory");   // the codes were written as other types than they are read
-      if (p.D_t) flush_t<TS, 16 * TI>(tl, r0, n0);
+      if (p.D_t) flush_t<TS, 16 * TI>(wl + codes_at, r0, n0);
     }
   }
 
@@ -200,7 +382,7 @@ struct EpWave {
     constexpr int LPC = ROWS / 16;
     const int q = lane % LPC;
     const int64_t m = r0 + 16 * q, left = p.M - m;
-#pragma unroll 4
+#pragma unroll 2
     for (int k = lane / LPC; k < WTN; k += 64 / LPC) {
       const int64_t n = n0 + k;
       if (n >= p.N || left <= 0) continue;
@@ -219,7 +401,7 @@ struct EpWave {
   // Column sums of the wavefront's rows to part[row][N] (row: which rows of
   // the sum these are), joined in a fixed order by k_ep_dbias.
   __device__ __forceinline__ void put_dbias(int64_t row) {
-    if (e.dbias == nullptr) return;
+    if (!backward() || e.dbias == nullptr) return;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
 #pragma unroll
@@ -241,6 +423,26 @@ struct EpWave {
       f(std::integral_constant<int, B>{});
       ep_for<B + 1, E>(f);
     }
+  }
+};
+
+template <int NW>
+__device__ __forceinline__ void ep_amax(float* d_amax, uint32_t bits, int lane, int wave);
+
+// The epilogue as the large kernels take it (FAST): accumulators of a wavefront whose
+// rows start at r0 and columns at c0; part: its row of column sums.
+template <int DIR>
+struct LinearEp {
+  EpParams e;
+  template <bool OUT8, int TI, int TJ, int NW, typename Deq>
+  __device__ __forceinline__ void finish(const GemmParams& p, const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0,
+                                         int64_t c0, int64_t part, int lane, int wave, uint8_t* wl) const {
+    using W = EpWave<16 * TJ, OUT8, DIR, true>;
+    static_assert(W::bytes(TI) <= 128 * 1024 / NW, "the wavefront's part of the stages");
+    W w(p, e, c0, lane);
+    w.template tile<TI, TJ>(acc, deq, r0, c0, wl);
+    w.put_dbias(part);
+    if (p.d_amax) ep_amax<NW>(p.d_amax, w.amax_bits(), lane, wave);
   }
 };
 

@@ -41,7 +41,8 @@ __global__ void __launch_bounds__(EP_THREADS) k_ep_tile(GemmParams p, EpParams e
   constexpr int SCALES = BLOCK ? 4 * ((BM_ + 63) / 64 * 64 + (BN_ + 63) / 64 * 64) : 0;
   constexpr int SA0 = ABYTES + BBYTES, SB0 = SA0 + (BM_ + 63) / 64 * 64 * 4;
   constexpr int STAGE_ = ABYTES + BBYTES + SCALES;
-  constexpr int WREG = 64 * 16 * TJ + (OUT8 ? 16 * TJ * (16 * TI + 16) : 0);   // epilogue bytes per wavefront
+  constexpr int WREG = EpWave<16 * TJ, OUT8, EP_ANY, false>::bytes(TI) > EpWave<16 * TJ, false, EP_ANY, false>::bytes(TI)
+                           ? EpWave<16 * TJ, OUT8, EP_ANY, false>::bytes(TI) : EpWave<16 * TJ, false, EP_ANY, false>::bytes(TI);
   constexpr int LDS_ = STAGES * STAGE_ > 4 * WREG ? STAGES * STAGE_ : 4 * WREG;
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_];
   __shared__ float rs_tab[BLOCK ? 1 : BM_ + BN_];
@@ -173,11 +174,11 @@ __global__ void __launch_bounds__(EP_THREADS) k_ep_tile(GemmParams p, EpParams e
     ps.ldd = e.ldw;
     ps.d_f32 = 1;
     ps.d_amax = nullptr;
-    EpWave<16 * TJ, false> w(ps, es, c0, lane);
+    EpWave<16 * TJ, false, EP_FWD, false> w(ps, es, c0, lane);
     w.template tile<TI, TJ>(acc, deq, r0, c0, wl);
     return;
   }
-  EpWave<16 * TJ, OUT8> w(p, e, c0, lane);
+  EpWave<16 * TJ, OUT8, EP_ANY, false> w(p, e, c0, lane);
   w.template tile<TI, TJ>(acc, deq, r0, c0, wl);
   w.put_dbias((int64_t)tm * WM + wm);
   if (p.d_amax) ep_amax<4>(p.d_amax, w.amax_bits(), lane, wave);

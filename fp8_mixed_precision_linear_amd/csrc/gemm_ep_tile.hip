@@ -11,31 +11,35 @@ namespace {
 template <bool OUT8>
 __global__ void __launch_bounds__(256) k_ep_join(GemmParams p, EpParams e) {
   constexpr int TS = 32;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[OUT8 ? 4 * 128 * TS : 16];
+  using W = EpWave<128, OUT8, EP_ANY, false>;
+  constexpr int BYTES = W::bytes(1), RPL = W::RPL;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t n0 = (int64_t)blockIdx.x * 128, m0 = (int64_t)blockIdx.y * 64 + 16 * wave;
-  EpWave<128, OUT8> w(p, e, n0, lane);
-  constexpr int RPL = EpWave<128, OUT8>::RPL;
-  float v[RPL][8], o[RPL][8];
+  uint8_t* wl = lds + wave * BYTES;
+  W w(p, e, n0, lane);
+  uint32_t o[RPL][W::SW];
   w.fetch(m0, o);
 #pragma unroll
   for (int t = 0; t < RPL; ++t) {
-    const int64_t m = m0 + w.rg * RPL + t;
-    const int n = m < p.M ? w.nv : 0;
+    const int r = w.rg * RPL + t;
+    const int64_t m = m0 + r;
+    const int n = m < p.M ? 8 : 0;   // (rows of the sums are padded to whole vectors)
+    float v[8] = {};
+    if (w.nv > 0)
+      for (int z = 0; z < e.splits; ++z) {
+        float s[8];
+        load8(e.sums, 1, ((int64_t)z * p.M + m) * e.ldw + w.c, n, s);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[t][k] = 0.0f;
-    for (int z = 0; z < e.splits; ++z) {
-      float s[8];
-      load8(e.sums, 1, ((int64_t)z * p.M + m) * e.ldw + w.c, n, s);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[t][k] += s[k];
-    }
+        for (int k = 0; k < 8; ++k) v[k] += s[k];
+      }
+    *w.place(wl, r, 2 * w.cq) = make_float4(v[0], v[1], v[2], v[3]);
+    *w.place(wl, r, 2 * w.cq + 1) = make_float4(v[4], v[5], v[6], v[7]);
   }
-  uint8_t* tl = lds + (OUT8 ? wave * 128 * TS : 0);
-  w.template strip<TS>(m0, v, o, tl, 0);
+  w.stage(m0, o, wl + W::src_at);
+  w.template rows<TS>(m0, wl, wl + W::src_at, wl + W::codes_at, 0);
   if constexpr (OUT8) {
-    asm volatile("" ::: "memory");
-    if (p.D_t) w.template flush_t<TS, 16>(tl, m0, n0);
+    if (p.D_t) w.template flush_t<TS, 16>(wl + W::codes_at, m0, n0);
   }
   w.put_dbias((int64_t)blockIdx.y * 4 + wave);
   if (p.d_amax) ep_amax<4>(p.d_amax, w.amax_bits(), lane, wave);
@@ -80,6 +84,10 @@ hipError_t launch_fmt(const GemmParams& p, const EpParams& e, const EpPlan& plan
 
 EpPlan ep_plan(const GemmParams& p) {
   EpPlan plan = {};
+  const int64_t big_tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
+  const bool layer = (p.a_scaling == 0 || p.a_scaling == 5) ? (p.b_scaling == 0 || p.b_scaling == 5)
+                     : p.a_scaling == 1 ? p.b_scaling == 2 : p.a_scaling == 3 ? p.b_scaling == 4 : false;
+  plan.large = layer && p.K > 0 && 2 * big_tiles >= device_cu_count();
   plan.bm = 128;
   plan.bn = 128;
   plan.splits = 1;
@@ -89,7 +97,8 @@ EpPlan ep_plan(const GemmParams& p) {
   // Split K while the tiles leave compute units without work and every part
   // keeps at least four steps.
   int64_t splits = 1;
-  while (splits < 16 && tiles * splits * 2 <= cu && nk / (splits * 2) >= 4) splits *= 2;
+  while (!plan.large && splits < 16 && tiles * splits * 2 <= cu && nk / (splits * 2) >= 4) splits *= 2;
+  if (plan.large) plan.parts = (p.M + 255) / 256 * 2;
   if (splits > 1) {
     plan.splits = (int)splits;
     plan.parts = (p.M + 63) / 64 * 4;   // wavefronts of the join
@@ -100,11 +109,21 @@ EpPlan ep_plan(const GemmParams& p) {
   return plan;
 }
 
+namespace {
+// The large kernels' formats, and rows of whole vectors that start on a dword
+// (see FAST in gemm_ep.h).
+bool large_takes(const GemmParams& p, const EpParams& e) {
+  auto dwords = [](const void* q, int64_t ld, int size) {
+    return q == nullptr || (((reinterpret_cast<uintptr_t>(q) & 3u) == 0) && ((ld * size) & 3) == 0);
+  };
+  return p.b_fmt == 0 && p.a_fmt == e.backward && p.N % 8 == 0 &&
+         dwords(p.D, p.ldd, p.d_fp8 ? 1 : (p.d_f32 ? 4 : 2)) && dwords(e.aux, e.ldaux, 2) &&
+         dwords(e.residual, e.ldres, e.res_f32 ? 4 : 2);
+}
+}  // namespace
+
 hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStream_t s) {
   GemmParams p = p0;
-  // power-of-two block scales are binary32 scales of the same layouts here
-  if (p.a_scaling == 3 || p.a_scaling == 4) p.a_scaling -= 2;
-  if (p.b_scaling == 3 || p.b_scaling == 4) p.b_scaling -= 2;
   if (p.d_amax && !p.amax_acc) {
     const hipError_t err = launch_fill_u32(reinterpret_cast<uint32_t*>(p.d_amax), 1, 0u, s);
     if (err != hipSuccess) return err;
@@ -115,10 +134,19 @@ hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStre
   e.sums = reinterpret_cast<float*>(ws + plan.part_bytes);
   e.ldw = plan.ldw;
   e.splits = plan.splits;
+  const bool large = plan.large && large_takes(p, e);
+  int64_t parts = plan.parts;
+  if (!large) {
+    // power-of-two block scales are binary32 scales of the same layouts here
+    if (p.a_scaling == 3 || p.a_scaling == 4) p.a_scaling -= 2;
+    if (p.b_scaling == 3 || p.b_scaling == 4) p.b_scaling -= 2;
+    if (plan.splits == 1) parts = (p.M + 127) / 128 * 2;
+  }
   const bool block = !((p.a_scaling == 0 || p.a_scaling == 5) && (p.b_scaling == 0 || p.b_scaling == 5));
   if (p.M > 0) {
     hipError_t err;
-    if (block) err = p.d_fp8 ? launch_fmt<true, true>(p, e, plan, s) : launch_fmt<true, false>(p, e, plan, s);
+    if (large) err = p.d_fp8 ? launch_gemm_ep_large_fp8out(p, e, s) : launch_gemm_ep_large(p, e, s);
+    else if (block) err = p.d_fp8 ? launch_fmt<true, true>(p, e, plan, s) : launch_fmt<true, false>(p, e, plan, s);
     else err = p.d_fp8 ? launch_fmt<false, true>(p, e, plan, s) : launch_fmt<false, false>(p, e, plan, s);
     if (err != hipSuccess) return err;
     if (plan.splits > 1) {
@@ -130,7 +158,7 @@ hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStre
     }
   }
   if (e.dbias) {
-    hipLaunchKernelGGL(k_ep_dbias, dim3((unsigned)((p.N + 63) / 64)), dim3(1024), 0, s, e.part, plan.parts, p.N,
+    hipLaunchKernelGGL(k_ep_dbias, dim3((unsigned)((p.N + 63) / 64)), dim3(1024), 0, s, e.part, parts, p.N,
                        e.dbias, e.bias_f32);
     return hipGetLastError();
   }

@@ -58,9 +58,11 @@ constexpr int W4_OUT8_PASSES = 2;
 // instruction, the accumulator staying in its C operand ([MPG] "DeepSeek
 // FP8 training recipe in detail > Block-wise scaling at 128 granularity";
 // a per-tensor operand's scale goes to the epilogue).
-template <int AF, int BF, bool KT, bool OUT8, int MODE>
+// EP: the linear's epilogue (gemm_ep.h) in place of the plain one, its arguments
+// in `ep` (NoEpilogue: none).
+template <int AF, int BF, bool KT, bool OUT8, int MODE, typename EP = NoEpilogue>
 __global__ void __launch_bounds__(W4_THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
-k_gemm_w4(GemmParams p, int tiles_m, int tiles_n) {
+k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   constexpr bool ROWS = MODE == W4_ROWS, MX = MODE >= W4_MX;
   constexpr bool SA_ROWS = MX && ((MODE - W4_MX) & 1), SB_COL = MX && ((MODE - W4_MX) & 2);
   static_assert(!(MX && KT), "block scales make K a multiple of the step");
@@ -318,6 +320,12 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n) {
     else
       return (x * sa) * sb;
   };
+  if constexpr (!std::is_same_v<EP, NoEpilogue>) {
+    __syncthreads();   // every wavefront is done reading both stages
+    ep.template finish<OUT8, 8, 8, 4>(p, acc, deq, m0 + wm * 128, n0 + wn * 128, tm * 2 + wm, lane, wave,
+                                      &lds[0][0] + wave * 32768);
+    return;
+  }
   const int esz = OUT8 ? 1 : (p.d_f32 ? 4 : 2);
   const bool staged = (m0 + BM <= M) && (n0 + BN <= N) && ((p.ldd * esz) % 16 == 0) &&
                       ((reinterpret_cast<uintptr_t>(p.D) & 15u) == 0) &&
@@ -343,11 +351,11 @@ hipError_t launch_w4_k(const GemmParams& p, hipStream_t s) {
   const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
   const dim3 grid((unsigned)(tiles_m * tiles_n)), block(W4_THREADS);
   if constexpr (MODE >= W4_MX)   // block scales: K is a multiple of the step
-    hipLaunchKernelGGL((k_gemm_w4<AF, BF, false, OUT8, MODE>), grid, block, 0, s, p, tiles_m, tiles_n);
+    hipLaunchKernelGGL((k_gemm_w4<AF, BF, false, OUT8, MODE>), grid, block, 0, s, p, tiles_m, tiles_n, NoEpilogue{});
   else if (p.K % BK == 0)
-    hipLaunchKernelGGL((k_gemm_w4<AF, BF, false, OUT8, MODE>), grid, block, 0, s, p, tiles_m, tiles_n);
+    hipLaunchKernelGGL((k_gemm_w4<AF, BF, false, OUT8, MODE>), grid, block, 0, s, p, tiles_m, tiles_n, NoEpilogue{});
   else
-    hipLaunchKernelGGL((k_gemm_w4<AF, BF, true, OUT8, MODE>), grid, block, 0, s, p, tiles_m, tiles_n);
+    hipLaunchKernelGGL((k_gemm_w4<AF, BF, true, OUT8, MODE>), grid, block, 0, s, p, tiles_m, tiles_n, NoEpilogue{});
   return hipGetLastError();
 }
 

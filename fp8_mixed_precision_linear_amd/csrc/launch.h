@@ -198,9 +198,14 @@ struct EpParams {
 // How a product is cut: tile, parts of K, rows of column sums, workspace.
 struct EpPlan {
   int bm, bn, splits;
+  bool large;   // 256 x 256 tiles of the large kernels
   int64_t parts, ldw, part_bytes, sums_bytes;
 };
 EpPlan ep_plan(const GemmParams& p);
+// Power-of-two scalings keep their codes in launch_gemm_ep_large*, are block
+// scales like any others in the tile kernels.
+hipError_t launch_gemm_ep_large(const GemmParams& p, const EpParams& e, hipStream_t s);
+hipError_t launch_gemm_ep_large_fp8out(const GemmParams& p, const EpParams& e, hipStream_t s);
 hipError_t launch_gemm_ep(const GemmParams& p, EpParams e, uint8_t* ws, hipStream_t s);
 
 }  // namespace fp8lin

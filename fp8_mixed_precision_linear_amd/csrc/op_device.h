@@ -381,44 +381,48 @@ __device__ __forceinline__ float gate_slope(int act, float value) {
 }
 
 // Activations of the linear's epilogue: 0 none, 1 ReLU, 2 GELU (erf),
-// 3 GELU (tanh form), 4 SiLU.  The sigmoid forms cost one exponential and one
-// reciprocal: the tanh form of GELU is u * sigmoid(2 t), t = sqrt(2/pi) (u +
-// 0.044715 u^3), because 0.5 (1 + tanh t) = sigmoid(2 t).
+// 3 GELU (tanh form), 4 SiLU; u -> act(u), or act'(u).
+// The sigmoid forms cost one exponential and one reciprocal: with s(x) = 1 /
+// (1 + e^-x), SiLU is u s(u) and the tanh form of GELU u s(2 t), t = sqrt(2/pi)
+// (u + 0.044715 u^3), because 0.5 (1 + tanh t) = s(2 t); both slopes are
+// s + u s (1 - s) x'(u).  erf is formula 7.1.26 of Abramowitz and Stegun,
+// "Handbook of Mathematical Functions" (absolute error below 1.5e-7, a unit of
+// binary32 near 1): one reciprocal and e^(-u^2/2), which the slope needs too.
 constexpr float kRootTwoOverPi = 0.797884560802865f;
-__device__ __forceinline__ float sigmoid_of_log2(float t) {   // 1 / (1 + 2^-t)
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-t));
+template <bool SLOPE>
+__device__ __forceinline__ float gelu_erf(float u) {
+  const float x = __builtin_fabsf(u) * 0.707106781186548f;
+  const float e = __builtin_amdgcn_exp2f(-0.5f * kLog2E * u * u);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+  float q = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
+  q = __builtin_fmaf(t, q, 1.421413741f);
+  q = __builtin_fmaf(t, q, -0.284496736f);
+  q = __builtin_fmaf(t, q, 0.254829592f);
+  const float tail = 0.5f * q * t * e;               // 0.5 (1 - erf x)
+  const float cdf = u < 0.0f ? tail : 1.0f - tail;   // 0.5 (1 + erf(u / sqrt 2))
+  return SLOPE ? __builtin_fmaf(u * 0.398942280401433f, e, cdf) : u * cdf;
 }
-template <int ACT>
-__device__ __forceinline__ float act_value(float u) {
-  if constexpr (ACT == 1) return u > 0.0f ? u : (u != u ? u : 0.0f);
-  if constexpr (ACT == 2) return 0.5f * u * (1.0f + erff(u * 0.707106781186548f));
-  if constexpr (ACT == 3) {
-    constexpr float c = 2.0f * kRootTwoOverPi * kLog2E;
-    return u * sigmoid_of_log2(u * (c + c * 0.044715f * u * u));
+// u s(x(u)), x(u) = u (a + b u^2).
+struct SigmoidForm {
+  float a, b;
+  __device__ __forceinline__ explicit SigmoidForm(int act)
+      : a(act == 3 ? 2.0f * kRootTwoOverPi : 1.0f), b(act == 3 ? 2.0f * kRootTwoOverPi * 0.044715f : 0.0f) {}
+  __device__ __forceinline__ float sigmoid(float u, float q) const {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f((-kLog2E * u) * __builtin_fmaf(b, q, a)));
   }
-  if constexpr (ACT == 4) return u * sigmoid_of_log2(u * kLog2E);
-  return u;
-}
-template <int ACT>
-__device__ __forceinline__ float act_slope(float u) {
-  if constexpr (ACT == 1) return u > 0.0f ? 1.0f : 0.0f;
-  if constexpr (ACT == 2)
-    return 0.5f * (1.0f + erff(u * 0.707106781186548f)) +
-           u * (0.398942280401433f * __builtin_amdgcn_exp2f(-0.5f * kLog2E * u * u));
-  if constexpr (ACT == 3) {
-    // d/du [u s(2t)] = s + u s (1 - s) 2 t'; beyond +-30 s is 1 or 0 and the
-    // second term 0, where u * u could overflow and give inf * 0
-    constexpr float c = 2.0f * kRootTwoOverPi;
-    u = u == u ? __builtin_amdgcn_fmed3f(u, -30.0f, 30.0f) : u;
-    const float s = sigmoid_of_log2(u * (c * kLog2E + c * kLog2E * 0.044715f * u * u));
-    return s + u * s * (1.0f - s) * (c + 3.0f * c * 0.044715f * u * u);
+  __device__ __forceinline__ float value(float u) const {
+    // (u^2 stays finite: b u^2 is far past where s is 1 or 0, and 0 * inf is NaN)
+    const float q = __builtin_fminf(u * u, 1e30f);
+    return u * sigmoid(u, q);
   }
-  if constexpr (ACT == 4) {
-    const float s = sigmoid_of_log2(u * kLog2E);
-    return s * (1.0f + u * (1.0f - s));
+  // s + u s (1 - s) x'(u); beyond +-100 s is 1 or 0 in both forms and u no
+  // longer matters, where u^2 might overflow into inf * 0.
+  __device__ __forceinline__ float slope(float u) const {
+    u = u == u ? __builtin_amdgcn_fmed3f(u, -100.0f, 100.0f) : u;
+    const float q = u * u, s = sigmoid(u, q);
+    return __builtin_fmaf(u * (s - s * s), __builtin_fmaf(3.0f * b, q, a), s);
   }
-  return 1.0f;
-}
+};
 
 }  // namespace
 

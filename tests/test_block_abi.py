@@ -78,7 +78,8 @@ def gemm_ep(L, ep=None, **kw):
     (dict(lda=1 << 24), {}, UNSUPPORTED), (dict(D_t=0x6000), {}, ARG), (dict(d_dtype=2), {}, NULL), ({}, dict(act=5), ARG),
     ({}, dict(backward=2), ARG), ({}, dict(param_dtype=3), ARG), ({}, dict(residual_dtype=3), ARG),
     ({}, dict(backward=1, bias=0x6000), ARG), ({}, dict(backward=1, residual=0x6000, ldres=16), ARG), ({}, dict(dbias=0x6000), ARG),
-    ({}, dict(backward=1, act=1), NULL), ({}, dict(aux=0x6000, ldaux=15), SHAPE), ({}, dict(residual=0x6000, ldres=15), SHAPE),
+    ({}, dict(backward=1, act=1), NULL), ({}, dict(aux=0x6000, ldaux=15), SHAPE),
+    (dict(d_dtype=2, d_scale=0x7000), dict(residual=0x6000, ldres=16, residual_dtype=1), UNSUPPORTED), ({}, dict(residual=0x6000, ldres=15), SHAPE),
     ({}, dict(workspace=None), NULL), ({}, dict(workspace_bytes=8), SHAPE), ({}, dict(workspace=0x10008), ALIGN),
     ({}, dict(bias=0x6001), ALIGN), ({}, dict(aux=0x6001, ldaux=16), ALIGN), (dict(M=0), {}, 0)])
 def test_gemm_ep(L, kw, ep, status):
