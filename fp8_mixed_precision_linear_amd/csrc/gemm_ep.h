@@ -189,6 +189,7 @@ template <int WTN, bool OUT8, int DIR, bool FAST>
 struct EpWave {
   static constexpr int LPR = WTN / 8;        // lanes per row
   static constexpr int RPL = WTN / 32;       // rows per lane and strip of 16
+  static_assert(RPL == 1 || RPL == 2 || RPL == 4, "32, 64 or 128 columns");
   static constexpr int CH = WTN / 4;         // 16-byte chunks of a strip's row
   static constexpr int SW = OUT8 ? (FAST ? 4 : 5) : 8;   // words of eight values of src in flight
   const GemmParams& p;
@@ -333,12 +334,9 @@ struct EpWave {
         uint8_t* dst = tl + (8 * cq) * TS + tr + rg * RPL;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          if constexpr (RPL == 4) {
-            *reinterpret_cast<uint32_t*>(dst + k * TS) = turned[k];
-          } else {
-            static_assert(RPL == 2, "two or four rows per lane");
-            *reinterpret_cast<uint16_t*>(dst + k * TS) = (uint16_t)(turned[k] >> 16);
-          }
+          if constexpr (RPL == 4) *reinterpret_cast<uint32_t*>(dst + k * TS) = turned[k];
+          else if constexpr (RPL == 2) *reinterpret_cast<uint16_t*>(dst + k * TS) = (uint16_t)(turned[k] >> 16);
+          else dst[k * TS] = (uint8_t)(turned[k] >> 24);
         }
       }
     }

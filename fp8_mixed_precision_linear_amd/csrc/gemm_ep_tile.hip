@@ -87,7 +87,8 @@ EpPlan ep_plan(const GemmParams& p) {
   const int64_t big_tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
   const bool layer = (p.a_scaling == 0 || p.a_scaling == 5) ? (p.b_scaling == 0 || p.b_scaling == 5)
                      : p.a_scaling == 1 ? p.b_scaling == 2 : p.a_scaling == 3 ? p.b_scaling == 4 : false;
-  plan.large = layer && p.K > 0 && 2 * big_tiles >= device_cu_count();
+  plan.large = p.M > 64 && layer && p.K > 0 && 2 * big_tiles >= device_cu_count();
+  plan.skinny = p.M <= 64;
   plan.bm = 128;
   plan.bn = 128;
   plan.splits = 1;
@@ -97,7 +98,8 @@ EpPlan ep_plan(const GemmParams& p) {
   // Split K while the tiles leave compute units without work and every part
   // keeps at least four steps.
   int64_t splits = 1;
-  while (!plan.large && splits < 16 && tiles * splits * 2 <= cu && nk / (splits * 2) >= 4) splits *= 2;
+  while (!plan.large && !plan.skinny && splits < 16 && tiles * splits * 2 <= cu && nk / (splits * 2) >= 4) splits *= 2;
+  if (plan.skinny) plan.parts = (p.M + 15) / 16;
   if (plan.large) plan.parts = (p.M + 255) / 256 * 2;
   if (splits > 1) {
     plan.splits = (int)splits;
@@ -140,12 +142,13 @@ hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStre
     // power-of-two block scales are binary32 scales of the same layouts here
     if (p.a_scaling == 3 || p.a_scaling == 4) p.a_scaling -= 2;
     if (p.b_scaling == 3 || p.b_scaling == 4) p.b_scaling -= 2;
-    if (plan.splits == 1) parts = (p.M + 127) / 128 * 2;
+    if (plan.splits == 1 && !plan.skinny) parts = (p.M + 127) / 128 * 2;
   }
   const bool block = !((p.a_scaling == 0 || p.a_scaling == 5) && (p.b_scaling == 0 || p.b_scaling == 5));
   if (p.M > 0) {
     hipError_t err;
     if (large) err = p.d_fp8 ? launch_gemm_ep_large_fp8out(p, e, s) : launch_gemm_ep_large(p, e, s);
+    else if (plan.skinny) err = p.d_fp8 ? launch_gemm_ep_skinny_fp8out(p, e, s) : launch_gemm_ep_skinny(p, e, s);
     else if (block) err = p.d_fp8 ? launch_fmt<true, true>(p, e, plan, s) : launch_fmt<true, false>(p, e, plan, s);
     else err = p.d_fp8 ? launch_fmt<false, true>(p, e, plan, s) : launch_fmt<false, false>(p, e, plan, s);
     if (err != hipSuccess) return err;

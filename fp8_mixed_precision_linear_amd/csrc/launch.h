@@ -199,6 +199,7 @@ struct EpParams {
 struct EpPlan {
   int bm, bn, splits;
   bool large;   // 256 x 256 tiles of the large kernels
+  bool skinny;  // few rows: weights streamed to registers
   int64_t parts, ldw, part_bytes, sums_bytes;
 };
 EpPlan ep_plan(const GemmParams& p);
@@ -206,6 +207,8 @@ EpPlan ep_plan(const GemmParams& p);
 // scales like any others in the tile kernels.
 hipError_t launch_gemm_ep_large(const GemmParams& p, const EpParams& e, hipStream_t s);
 hipError_t launch_gemm_ep_large_fp8out(const GemmParams& p, const EpParams& e, hipStream_t s);
+hipError_t launch_gemm_ep_skinny(const GemmParams& p, const EpParams& e, hipStream_t s);
+hipError_t launch_gemm_ep_skinny_fp8out(const GemmParams& p, const EpParams& e, hipStream_t s);
 hipError_t launch_gemm_ep(const GemmParams& p, EpParams e, uint8_t* ws, hipStream_t s);
 
 }  // namespace fp8lin
