@@ -4,9 +4,9 @@
 //
 // A workgroup owns 32 columns; its eight wavefronts take every eighth 128-byte
 // step of K each.  Weights go from memory straight into the registers that feed
-// the matrix instruction: lane (g, l16) reads the 32 bytes at 32 g of row l16, so
-// the four lanes of a row cover its line, and A's fragments (from L2: A is small
-// and shared) take the same bytes of K.  U steps are in flight per wavefront, each
+// the matrix instruction: lane (g, l16) reads 16 bytes at 16 g and 16 at
+// 64 + 16 g of row l16, so the four lanes of a row read 64 bytes in a piece, and A's
+// fragments (from L2: A is small and shared) take the same bytes of K.  U steps are in flight per wavefront, each
 // reloaded as soon as its products are issued, so a compute unit keeps
 // 8 U 4 KB = 128 KB of weights under way; there is no barrier until the end, where
 // the wavefronts' sums are added in order through LDS and MT wavefronts apply the
@@ -47,9 +47,9 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
   const uint8_t* arow[MT];
   const uint8_t* brow[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) arow[i] = p.A + min((int64_t)(16 * i + l16), M - 1) * p.lda + 32 * g;
+  for (int i = 0; i < MT; ++i) arow[i] = p.A + min((int64_t)(16 * i + l16), M - 1) * p.lda + 16 * g;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) brow[j] = p.B + min(n0 + 16 * j + l16, N - 1) * p.ldb + 32 * g;
+  for (int j = 0; j < NT; ++j) brow[j] = p.B + min(n0 + 16 * j + l16, N - 1) * p.ldb + 16 * g;
   // block scales: A's of this lane's row, B's of its 4 columns or of the block
   const float* asc[MT];
   const float* bsc[NT][SBCOL ? 4 : 1];
@@ -68,14 +68,14 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
     v8i a[MT], b[NT];
     float sa[BLOCK ? MT : 1], sb[BLOCK ? NT : 1][SBCOL ? 4 : 1];
   };
-  auto line = [&](const uint8_t* row, int k) -> v8i {   // 32 bytes at k, zeros past K (a multiple of 16)
+  auto line = [&](const uint8_t* row, int k) -> v8i {   // zeros past K (a multiple of 16)
     uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-    if (k + 32 * g < K) lo = *reinterpret_cast<const uint4*>(row + k);
-    if (k + 32 * g + 16 < K) hi = *reinterpret_cast<const uint4*>(row + k + 16);
+    if (k + 16 * g < K) lo = *reinterpret_cast<const uint4*>(row + k);
+    if (k + 16 * g + 64 < K) hi = *reinterpret_cast<const uint4*>(row + k + 64);
     return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
   };
   auto whole = [&](const uint8_t* row, int k) -> v8i {
-    const uint4 lo = *reinterpret_cast<const uint4*>(row + k), hi = *reinterpret_cast<const uint4*>(row + k + 16);
+    const uint4 lo = *reinterpret_cast<const uint4*>(row + k), hi = *reinterpret_cast<const uint4*>(row + k + 64);
     return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
   };
   auto load = [&](int kb, Step& s) {

@@ -117,16 +117,21 @@ __global__ void __launch_bounds__(EP_THREADS) k_ep_tile(GemmParams p, EpParams e
     }
   }
 
+  // STAGES - 1 stages ahead; a step waits for its own stage only (the stages after
+  // it were issued later, PL instructions each, and may still be on their way).
+  constexpr int PL = QA + QB + (BLOCK ? ((BM_ + 63) / 64 + (BN_ + 63) / 64 + 3) / 4 : 0);
+  static_assert((STAGES - 2) * PL < 64, "counter of outstanding loads");
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s)
     if (kb0 + s < kb1) load(kb0 + s, s);
-  for (int kb = kb0; kb < kb1; ++kb) {
-    const int st = (kb - kb0) % STAGES;
+  int st = 0;
+  for (int kb = kb0; kb < kb1; ++kb, st = st + 1 == STAGES ? 0 : st + 1) {
     // Every wavefront's share of this step's stage has to be in LDS, and every
     // wavefront done with the stage that the next load fills.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    if (kb + STAGES - 2 < kb1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((STAGES - 2) * PL) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __syncthreads();
-    if (kb + STAGES - 1 < kb1) load(kb + STAGES - 1, (st + STAGES - 1) % STAGES);
+    if (kb + STAGES - 1 < kb1) load(kb + STAGES - 1, st == 0 ? STAGES - 1 : st - 1);
     const uint8_t* S = lds + st * STAGE_;
     v8i b[TJ];
 #pragma unroll
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(EP_THREADS) k_ep_tile(GemmParams p, EpParams e
   }
   EpWave<16 * TJ, OUT8, EP_ANY, false> w(p, e, c0, lane);
   w.template tile<TI, TJ>(acc, deq, r0, c0, wl);
-  w.put_dbias((int64_t)tm * WM + wm);
+  w.put_dbias((int64_t)tm * WM + wm);   // (rows of the sum: WM per tile-row)
   if (p.d_amax) ep_amax<4>(p.d_amax, w.amax_bits(), lane, wave);
 }
 

@@ -6,42 +6,40 @@ namespace fp8lin {
 
 namespace {
 
-// The parts' sums added in order, then the epilogue: a wavefront takes 16 rows
-// of 128 columns, a workgroup 64 rows.
+// The parts' sums added in order, then the epilogue: a wavefront takes 16 rows of
+// 32 columns (one row of 8 columns per lane), a workgroup 16 rows of 128.
 template <bool OUT8>
 __global__ void __launch_bounds__(256) k_ep_join(GemmParams p, EpParams e) {
   constexpr int TS = 32;
-  using W = EpWave<128, OUT8, EP_ANY, false>;
-  constexpr int BYTES = W::bytes(1), RPL = W::RPL;
+  using W = EpWave<32, OUT8, EP_ANY, false>;
+  constexpr int BYTES = W::bytes(1);
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n0 = (int64_t)blockIdx.x * 128, m0 = (int64_t)blockIdx.y * 64 + 16 * wave;
+  const int64_t n0 = (int64_t)blockIdx.x * 128 + 32 * wave, m0 = (int64_t)blockIdx.y * 16;
   uint8_t* wl = lds + wave * BYTES;
   W w(p, e, n0, lane);
-  uint32_t o[RPL][W::SW];
+  uint32_t o[1][W::SW];
   w.fetch(m0, o);
-#pragma unroll
-  for (int t = 0; t < RPL; ++t) {
-    const int r = w.rg * RPL + t;
-    const int64_t m = m0 + r;
-    const int n = m < p.M ? 8 : 0;   // (rows of the sums are padded to whole vectors)
-    float v[8] = {};
-    if (w.nv > 0)
-      for (int z = 0; z < e.splits; ++z) {
-        float s[8];
-        load8(e.sums, 1, ((int64_t)z * p.M + m) * e.ldw + w.c, n, s);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += s[k];
-      }
-    *w.place(wl, r, 2 * w.cq) = make_float4(v[0], v[1], v[2], v[3]);
-    *w.place(wl, r, 2 * w.cq + 1) = make_float4(v[4], v[5], v[6], v[7]);
+  const int64_t m = m0 + w.rg;
+  float v[8] = {};
+  if (w.nv > 0 && m < p.M) {   // (rows of the sums are padded to whole vectors)
+    const float* s = e.sums + m * e.ldw + w.c;
+    const int64_t next = p.M * e.ldw;
+#pragma unroll 8
+    for (int z = 0; z < e.splits; ++z) {
+      const float4 a = *reinterpret_cast<const float4*>(s + z * next), b = *reinterpret_cast<const float4*>(s + z * next + 4);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
   }
+  *w.place(wl, w.rg, 2 * w.cq) = make_float4(v[0], v[1], v[2], v[3]);
+  *w.place(wl, w.rg, 2 * w.cq + 1) = make_float4(v[4], v[5], v[6], v[7]);
   w.stage(m0, o, wl + W::src_at);
   w.template rows<TS>(m0, wl, wl + W::src_at, wl + W::codes_at, 0);
   if constexpr (OUT8) {
     if (p.D_t) w.template flush_t<TS, 16>(wl + W::codes_at, m0, n0);
   }
-  w.put_dbias((int64_t)blockIdx.y * 4 + wave);
+  w.put_dbias(blockIdx.y);
   if (p.d_amax) ep_amax<4>(p.d_amax, w.amax_bits(), lane, wave);
 }
 
@@ -68,7 +66,12 @@ template <int AF, int BF, bool BLOCK, bool OUT8>
 hipError_t launch_tile(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s) {
   const int tiles_m = (int)((p.M + plan.bm - 1) / plan.bm), tiles_n = (int)((p.N + plan.bn - 1) / plan.bn);
   const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)plan.splits), block(EP_THREADS);
-  hipLaunchKernelGGL((k_ep_tile<AF, BF, BLOCK, OUT8, 2, 2, 4, 4, 2>), grid, block, 0, s, p, e, tiles_m, tiles_n);
+  if (plan.bm == 32)
+    hipLaunchKernelGGL((k_ep_tile<AF, BF, BLOCK, OUT8, 1, 4, 2, 2, 6>), grid, block, 0, s, p, e, tiles_m, tiles_n);
+  else if (plan.bm == 64)
+    hipLaunchKernelGGL((k_ep_tile<AF, BF, BLOCK, OUT8, 2, 2, 2, 4, 5>), grid, block, 0, s, p, e, tiles_m, tiles_n);
+  else
+    hipLaunchKernelGGL((k_ep_tile<AF, BF, BLOCK, OUT8, 2, 2, 4, 4, 4>), grid, block, 0, s, p, e, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
@@ -82,31 +85,34 @@ hipError_t launch_fmt(const GemmParams& p, const EpParams& e, const EpPlan& plan
 
 }  // namespace
 
+namespace {
+int64_t tile_parts(int64_t M, int bm) { return (M + bm - 1) / bm * (bm == 32 ? 1 : 2); }
+}  // namespace
+
 EpPlan ep_plan(const GemmParams& p) {
   EpPlan plan = {};
   const int64_t big_tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
   const bool layer = (p.a_scaling == 0 || p.a_scaling == 5) ? (p.b_scaling == 0 || p.b_scaling == 5)
                      : p.a_scaling == 1 ? p.b_scaling == 2 : p.a_scaling == 3 ? p.b_scaling == 4 : false;
   plan.large = p.M > 64 && layer && p.K > 0 && 2 * big_tiles >= device_cu_count();
-  plan.skinny = p.M <= 64;
-  plan.bm = 128;
+  plan.skinny = p.M <= 16;
+  plan.bm = p.M <= 32 ? 32 : (p.M <= 64 ? 64 : 128);
   plan.bn = 128;
   plan.splits = 1;
-  plan.parts = (p.M + 127) / 128 * 2;   // wavefront rows of the tiles
-  const int64_t tiles = ((p.M + 127) / 128) * ((p.N + 127) / 128), cu = device_cu_count();
+  const int64_t tiles = ((p.M + plan.bm - 1) / plan.bm) * ((p.N + 127) / 128), cu = device_cu_count();
   const int64_t nk = (p.K + BK - 1) / BK;
   // Split K while the tiles leave compute units without work and every part
   // keeps at least four steps.
   int64_t splits = 1;
   while (!plan.large && !plan.skinny && splits < 16 && tiles * splits * 2 <= cu && nk / (splits * 2) >= 4) splits *= 2;
-  if (plan.skinny) plan.parts = (p.M + 15) / 16;
-  if (plan.large) plan.parts = (p.M + 255) / 256 * 2;
-  if (splits > 1) {
-    plan.splits = (int)splits;
-    plan.parts = (p.M + 63) / 64 * 4;   // wavefronts of the join
-  }
+  plan.splits = (int)splits;
+  // rows of column sums: the wavefronts' rows of tiles, or of the join
+  plan.parts = splits > 1 || plan.skinny ? (p.M + 15) / 16
+               : plan.large ? (p.M + 255) / 256 * 2 : tile_parts(p.M, plan.bm);
   plan.ldw = (p.N + 7) / 8 * 8;
-  plan.part_bytes = (plan.parts * p.N * 4 + 255) / 256 * 256;
+  // (a product of the large kernels' size may still run on the tiles: large_takes)
+  const int64_t parts = plan.large && tile_parts(p.M, plan.bm) > plan.parts ? tile_parts(p.M, plan.bm) : plan.parts;
+  plan.part_bytes = (parts * p.N * 4 + 255) / 256 * 256;
   plan.sums_bytes = plan.splits > 1 ? plan.splits * p.M * plan.ldw * 4 : 0;
   return plan;
 }
@@ -142,7 +148,7 @@ hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStre
     // power-of-two block scales are binary32 scales of the same layouts here
     if (p.a_scaling == 3 || p.a_scaling == 4) p.a_scaling -= 2;
     if (p.b_scaling == 3 || p.b_scaling == 4) p.b_scaling -= 2;
-    if (plan.splits == 1 && !plan.skinny) parts = (p.M + 127) / 128 * 2;
+    if (plan.large) parts = tile_parts(p.M, plan.bm);
   }
   const bool block = !((p.a_scaling == 0 || p.a_scaling == 5) && (p.b_scaling == 0 || p.b_scaling == 5));
   if (p.M > 0) {
@@ -153,7 +159,7 @@ hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStre
     else err = p.d_fp8 ? launch_fmt<false, true>(p, e, plan, s) : launch_fmt<false, false>(p, e, plan, s);
     if (err != hipSuccess) return err;
     if (plan.splits > 1) {
-      const dim3 grid((unsigned)((p.N + 127) / 128), (unsigned)((p.M + 63) / 64));
+      const dim3 grid((unsigned)((p.N + 127) / 128), (unsigned)((p.M + 15) / 16));
       if (p.d_fp8) hipLaunchKernelGGL((k_ep_join<true>), grid, dim3(256), 0, s, p, e);
       else hipLaunchKernelGGL((k_ep_join<false>), grid, dim3(256), 0, s, p, e);
       err = hipGetLastError();
