@@ -62,57 +62,73 @@ __global__ void __launch_bounds__(1024) k_ep_dbias(const float* part, int64_t pa
   else reinterpret_cast<uint16_t*>(dbias)[n] = f32_to_bf16_rne(s);
 }
 
-template <int AF, int BF, bool BLOCK, bool OUT8>
-hipError_t launch_tile(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s) {
-  const int tiles_m = (int)((p.M + plan.bm - 1) / plan.bm), tiles_n = (int)((p.N + plan.bn - 1) / plan.bn);
-  const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)plan.splits), block(EP_THREADS);
-  if (plan.bm == 32)
-    hipLaunchKernelGGL((k_ep_tile<AF, BF, BLOCK, OUT8, 1, 4, 2, 2, 6>), grid, block, 0, s, p, e, tiles_m, tiles_n);
-  else if (plan.bm == 64)
-    hipLaunchKernelGGL((k_ep_tile<AF, BF, BLOCK, OUT8, 2, 2, 2, 4, 5>), grid, block, 0, s, p, e, tiles_m, tiles_n);
-  else
-    hipLaunchKernelGGL((k_ep_tile<AF, BF, BLOCK, OUT8, 2, 2, 4, 4, 4>), grid, block, 0, s, p, e, tiles_m, tiles_n);
-  return hipGetLastError();
-}
-
-template <bool BLOCK, bool OUT8>
-hipError_t launch_fmt(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s) {
-  if (p.a_fmt == 0 && p.b_fmt == 0) return launch_tile<0, 0, BLOCK, OUT8>(p, e, plan, s);
-  if (p.a_fmt == 1 && p.b_fmt == 0) return launch_tile<1, 0, BLOCK, OUT8>(p, e, plan, s);
-  if (p.a_fmt == 0 && p.b_fmt == 1) return launch_tile<0, 1, BLOCK, OUT8>(p, e, plan, s);
-  return launch_tile<1, 1, BLOCK, OUT8>(p, e, plan, s);
-}
-
 }  // namespace
 
 namespace {
+
+// Times (us) of one 128-byte step of K, measured with every compute unit busy: a
+// workgroup alone on its compute unit, and two of them (the 32-row tiles' stages
+// fill its LDS).  Without and with block scales; 256: the large kernels.
+struct TileCost {
+  int bm;
+  float alone, two;
+};
+constexpr TileCost kCost[2][4] = {{{32, 0.35f, 0.0f}, {64, 0.44f, 0.64f}, {128, 0.74f, 0.95f}, {256, 1.45f, 0.0f}},
+                                  {{32, 0.50f, 0.0f}, {64, 0.66f, 0.92f}, {128, 1.15f, 1.50f}, {256, 1.75f, 0.0f}}};
+
+// What a product takes on tiles of c.bm rows with K in `splits` parts: a launch
+// and an epilogue, rounds of as many workgroups as run at once, and for parts a
+// second launch and the sums' way through memory.
+float tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int splits, int64_t cu) {
+  const int64_t bn = c.bm == 256 ? 256 : 128;
+  const int64_t wgs = (M + c.bm - 1) / c.bm * ((N + bn - 1) / bn) * splits;
+  const int64_t at_once = c.two > 0.0f ? 2 * cu : cu, full = wgs / at_once, rest = wgs - full * at_once;
+  const float round = c.two > 0.0f ? c.two : c.alone;
+  const float steps = (float)((nk + splits - 1) / splits);
+  float t = 5.0f + steps * ((float)full * round + (rest == 0 ? 0.0f : (rest <= cu ? c.alone : round)));
+  if (splits > 1) t += 5.0f + (float)(splits * M * N) * 8.0f / 3.5e6f;
+  return t;
+}
 int64_t tile_parts(int64_t M, int bm) { return (M + bm - 1) / bm * (bm == 32 ? 1 : 2); }
+
 }  // namespace
 
+// Up to 16 rows: the few-row kernel (16 x 8192 x 8192: 19.9 us against 26 on
+// tiles).  Beyond: the cut that the measured steps above make shortest.  Over 72
+// products (48 to 1500 rows, 1024 to 14336 columns, K 2304 to 8192, per-tensor and
+// block scales) it took 2% more than the fastest of all cuts on average, 24% at
+// worst (300 x 1024 x 4096, 16.1 us against 13.0).
 EpPlan ep_plan(const GemmParams& p) {
   EpPlan plan = {};
-  const int64_t big_tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  const bool layer = (p.a_scaling == 0 || p.a_scaling == 5) ? (p.b_scaling == 0 || p.b_scaling == 5)
-                     : p.a_scaling == 1 ? p.b_scaling == 2 : p.a_scaling == 3 ? p.b_scaling == 4 : false;
-  plan.large = p.M > 64 && layer && p.K > 0 && 2 * big_tiles >= device_cu_count();
+  const bool per_a = p.a_scaling == 0 || p.a_scaling == 5, per_b = p.b_scaling == 0 || p.b_scaling == 5;
+  const bool layer = per_a ? per_b : p.a_scaling == 1 ? p.b_scaling == 2 : p.a_scaling == 3 ? p.b_scaling == 4 : false;
+  const int64_t cu = device_cu_count(), nk = (p.K + BK - 1) / BK;
   plan.skinny = p.M <= 16;
-  plan.bm = p.M <= 32 ? 32 : (p.M <= 64 ? 64 : 128);
+  plan.bm = 32;
   plan.bn = 128;
   plan.splits = 1;
-  const int64_t tiles = ((p.M + plan.bm - 1) / plan.bm) * ((p.N + 127) / 128), cu = device_cu_count();
-  const int64_t nk = (p.K + BK - 1) / BK;
-  // Split K while the tiles leave compute units without work and every part
-  // keeps at least four steps.
-  int64_t splits = 1;
-  while (!plan.large && !plan.skinny && splits < 16 && tiles * splits * 2 <= cu && nk / (splits * 2) >= 4) splits *= 2;
-  plan.splits = (int)splits;
-  // rows of column sums: the wavefronts' rows of tiles, or of the join
-  plan.parts = splits > 1 || plan.skinny ? (p.M + 15) / 16
-               : plan.large ? (p.M + 255) / 256 * 2 : tile_parts(p.M, plan.bm);
+  if (!plan.skinny) {
+    const TileCost* cost = kCost[per_a && per_b ? 0 : 1];
+    float best = 0.0f;
+    for (int i = 0; i < 3; ++i)
+      for (int splits = 1; splits <= 16 && (splits == 1 || nk / splits >= 2); splits *= 2) {
+        const float t = tile_time(cost[i], p.M, p.N, nk, splits, cu);
+        if (best != 0.0f && t >= best) continue;
+        best = t;
+        plan.bm = cost[i].bm;
+        plan.splits = splits;
+      }
+    plan.large = layer && p.K > 0 && tile_time(cost[3], p.M, p.N, nk, 1, cu) < best;
+  }
+  // Rows of column sums: the wavefronts' of the tiles, of the join or of the
+  // few-row kernel; room for the tiles' too where a product of the large kernels'
+  // size may run on them (large_takes).
+  const int64_t tiled = plan.splits > 1 || plan.skinny ? (p.M + 15) / 16 : tile_parts(p.M, plan.bm);
+  const int64_t large = plan.large ? (p.M + 255) / 256 * 2 : 0;
+  plan.parts = tiled;
+  plan.large_parts = large;
   plan.ldw = (p.N + 7) / 8 * 8;
-  // (a product of the large kernels' size may still run on the tiles: large_takes)
-  const int64_t parts = plan.large && tile_parts(p.M, plan.bm) > plan.parts ? tile_parts(p.M, plan.bm) : plan.parts;
-  plan.part_bytes = (parts * p.N * 4 + 255) / 256 * 256;
+  plan.part_bytes = ((tiled > large ? tiled : large) * p.N * 4 + 255) / 256 * 256;
   plan.sums_bytes = plan.splits > 1 ? plan.splits * p.M * plan.ldw * 4 : 0;
   return plan;
 }
@@ -130,6 +146,10 @@ bool large_takes(const GemmParams& p, const EpParams& e) {
 }
 }  // namespace
 
+hipError_t launch_gemm_ep_tile(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s) {
+  return launch_tile_sum<false>(p, e, plan, s);
+}
+
 hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStream_t s) {
   GemmParams p = p0;
   if (p.d_amax && !p.amax_acc) {
@@ -141,24 +161,25 @@ hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStre
   e.part = reinterpret_cast<float*>(ws);
   e.sums = reinterpret_cast<float*>(ws + plan.part_bytes);
   e.ldw = plan.ldw;
-  e.splits = plan.splits;
   const bool large = plan.large && large_takes(p, e);
-  int64_t parts = plan.parts;
+  e.splits = large ? 1 : plan.splits;
+  const int64_t parts = large ? plan.large_parts : plan.parts;
+  // Power-of-two block scales on every block-scaled operand go into the matrix
+  // instruction; beside others they are binary32 scales of the same layouts, as
+  // they are for the few-row kernel (bound by memory, not by the promotion).
+  const bool promoted = p.a_scaling == 1 || p.a_scaling == 2 || p.b_scaling == 1 || p.b_scaling == 2;
   if (!large) {
-    // power-of-two block scales are binary32 scales of the same layouts here
     if (p.a_scaling == 3 || p.a_scaling == 4) p.a_scaling -= 2;
     if (p.b_scaling == 3 || p.b_scaling == 4) p.b_scaling -= 2;
-    if (plan.large) parts = tile_parts(p.M, plan.bm);
   }
-  const bool block = !((p.a_scaling == 0 || p.a_scaling == 5) && (p.b_scaling == 0 || p.b_scaling == 5));
   if (p.M > 0) {
     hipError_t err;
     if (large) err = p.d_fp8 ? launch_gemm_ep_large_fp8out(p, e, s) : launch_gemm_ep_large(p, e, s);
     else if (plan.skinny) err = p.d_fp8 ? launch_gemm_ep_skinny_fp8out(p, e, s) : launch_gemm_ep_skinny(p, e, s);
-    else if (block) err = p.d_fp8 ? launch_fmt<true, true>(p, e, plan, s) : launch_fmt<true, false>(p, e, plan, s);
-    else err = p.d_fp8 ? launch_fmt<false, true>(p, e, plan, s) : launch_fmt<false, false>(p, e, plan, s);
+    else if (promoted) err = p.d_fp8 ? launch_gemm_ep_tile_blk_fp8out(p, e, plan, s) : launch_gemm_ep_tile_blk(p, e, plan, s);
+    else err = p.d_fp8 ? launch_gemm_ep_tile_fp8out(p, e, plan, s) : launch_gemm_ep_tile(p, e, plan, s);
     if (err != hipSuccess) return err;
-    if (plan.splits > 1) {
+    if (e.splits > 1) {
       const dim3 grid((unsigned)((p.N + 127) / 128), (unsigned)((p.M + 15) / 16));
       if (p.d_fp8) hipLaunchKernelGGL((k_ep_join<true>), grid, dim3(256), 0, s, p, e);
       else hipLaunchKernelGGL((k_ep_join<false>), grid, dim3(256), 0, s, p, e);

@@ -1,0 +1,12 @@
+// gemm_ep_tile_blk.hip -- the tile kernels with the linear's epilogue, promoted
+// block scales, BF16 / FP32 output
+// (a translation unit of its own, compiled beside the others).
+#include "gemm_ep_tile.h"
+
+namespace fp8lin {
+
+hipError_t launch_gemm_ep_tile_blk(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s) {
+  return launch_tile_blk<false>(p, e, plan, s);
+}
+
+}  // namespace fp8lin

@@ -200,13 +200,18 @@ struct EpPlan {
   int bm, bn, splits;
   bool large;   // 256 x 256 tiles of the large kernels
   bool skinny;  // few rows: weights streamed to registers
-  int64_t parts, ldw, part_bytes, sums_bytes;
+  int64_t parts, large_parts;   // rows of column sums, off and on the large kernels
+  int64_t ldw, part_bytes, sums_bytes;
 };
 EpPlan ep_plan(const GemmParams& p);
 // Power-of-two scalings keep their codes in launch_gemm_ep_large*, are block
 // scales like any others in the tile kernels.
 hipError_t launch_gemm_ep_large(const GemmParams& p, const EpParams& e, hipStream_t s);
 hipError_t launch_gemm_ep_large_fp8out(const GemmParams& p, const EpParams& e, hipStream_t s);
+hipError_t launch_gemm_ep_tile(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s);
+hipError_t launch_gemm_ep_tile_fp8out(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s);
+hipError_t launch_gemm_ep_tile_blk(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s);
+hipError_t launch_gemm_ep_tile_blk_fp8out(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s);
 hipError_t launch_gemm_ep_skinny(const GemmParams& p, const EpParams& e, hipStream_t s);
 hipError_t launch_gemm_ep_skinny_fp8out(const GemmParams& p, const EpParams& e, hipStream_t s);
 hipError_t launch_gemm_ep(const GemmParams& p, EpParams e, uint8_t* ws, hipStream_t s);
