@@ -31,6 +31,50 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeParams p) {
   const int np = (int)p.pairs;
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens_wg;
   const int nt = (int)(p.tokens - t0 < p.tokens_wg ? p.tokens - t0 : p.tokens_wg);
+  // Units of a head: two vectors of 8 elements each.  Half layout: elements i0 ..
+  // and np + i0 ..; interleaved, and the elements past rot (other buffer than the
+  // input): vectors w and w + half the number of them, so that neighbouring lanes
+  // read neighbouring vectors.
+  const bool halves = !p.interleaved;
+  const int rest = p.copy_rest ? (int)p.dim - 2 * np : 0;
+  const int pu = halves ? (np + 7) / 8 : (2 * np + 15) / 16, ru = (rest + 15) / 16, units = pu + ru;
+  const int64_t heads = p.q_heads + p.k_heads, h0 = (int64_t)blockIdx.y * p.heads_wg;
+  const int nh = (int)(heads - h0 < p.heads_wg ? heads - h0 : p.heads_wg);
+  const int all = nt * nh * units;
+  // u / d for u, d < 2^16 (see launch_rope): exact, as u (d - 2^32 mod d) < 2^32
+  const uint32_t per_unit = 0xFFFFFFFFu / (uint32_t)units + 1u, per_head = 0xFFFFFFFFu / (uint32_t)nh + 1u;
+  constexpr int ES = F32 ? 4 : 2;
+  float x[2][8], y[2][8];
+  char* dst[2];
+  int w[2], tk[2], n[2], n2[2], second[2];   // unit of the head, token, elements of each vector, from first to second
+  auto fetch = [&](int u0) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int u = u0 + q * kRopeThreads, uc = u < all ? u : 0;
+      const int th = units == 1 ? uc : (int)__umulhi((uint32_t)uc, per_unit);
+      w[q] = uc - th * units;
+      tk[q] = nh == 1 ? th : (int)__umulhi((uint32_t)th, per_head);
+      int64_t h = h0 + (th - tk[q] * nh);
+      const int64_t tok = t0 + tk[q];
+      const bool is_k = h >= p.q_heads;
+      if (is_k) h -= p.q_heads;
+      const char* src = reinterpret_cast<const char*>(is_k ? p.k : p.q) +
+                        (tok * (is_k ? p.k_st : p.q_st) + h * (is_k ? p.k_sh : p.q_sh)) * ES;
+      dst[q] = reinterpret_cast<char*>(is_k ? p.k_out : p.q_out) +
+               (tok * (is_k ? p.ko_st : p.qo_st) + h * (is_k ? p.ko_sh : p.qo_sh)) * ES;
+      const bool turned = w[q] < pu;
+      const int first = turned ? 8 * w[q] : 2 * np + 8 * (w[q] - pu);
+      const int end = !turned ? (int)p.dim : (halves ? np : 2 * np);
+      second[q] = !turned ? 8 * ru : (halves ? np : 8 * pu);
+      n[q] = u < all ? end - first : 0;
+      n2[q] = turned && halves ? n[q] : n[q] - second[q];
+      dst[q] += first * ES;
+      load8(src, F32, first, n[q], x[q]);
+      load8(src, F32, first + second[q], n2[q], y[q]);
+    }
+  };
+  // the first units' elements are on their way while the angles are computed
+  fetch(threadIdx.x);
   for (int a = threadIdx.x; a < nt * np; a += kRopeThreads) {
     const int t = a / np, i = a - t * np;
     const int64_t tok = t0 + t;
@@ -45,66 +89,34 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeParams p) {
     cs[a] = make_float2(c * p.scale, s * p.scale);
   }
   __syncthreads();
-  // units of a head: 8 pairs each, then (other buffer than the input) the
-  // elements past rot, 16 each
-  const int pu = (np + 7) / 8, rest = (int)p.dim - 2 * np;
-  const int cu = p.copy_rest ? (rest + 15) / 16 : 0;
-  const int units = pu + cu;
-  const int64_t heads = p.q_heads + p.k_heads;
-  const int64_t h0 = (int64_t)blockIdx.y * p.heads_wg;
-  const int nh = (int)(heads - h0 < p.heads_wg ? heads - h0 : p.heads_wg);
-  const int all = nt * nh * units;
-  for (int u = threadIdx.x; u < all; u += kRopeThreads) {
-    const int th = u / units, w = u - th * units;
-    const int t = th / nh;
-    const int64_t tok = t0 + t;
-    int64_t h = h0 + (th - t * nh);
-    const bool is_k = h >= p.q_heads;
-    if (is_k) h -= p.q_heads;
-    const void* src = is_k ? p.k : p.q;
-    void* dst = is_k ? p.k_out : p.q_out;
-    const int64_t si = tok * (is_k ? p.k_st : p.q_st) + h * (is_k ? p.k_sh : p.q_sh);
-    const int64_t di = tok * (is_k ? p.ko_st : p.qo_st) + h * (is_k ? p.ko_sh : p.qo_sh);
-    if (w >= pu) {
-      const int e = 2 * np + 16 * (w - pu), left = (int)p.dim - e;
-      float v[8], v2[8];
-      load8(src, F32, si + e, left, v);
-      load8(src, F32, si + e + 8, left - 8, v2);
-      store8(dst, F32, di + e, left, v);
-      store8(dst, F32, di + e + 8, left - 8, v2);
-      continue;
-    }
-    const int i0 = 8 * w, n = np - i0 < 8 ? np - i0 : 8;
-    const float2* a = cs + t * np + i0;
-    float x[8], y[8];
-    if (p.interleaved) {
-      load8(src, F32, si + 2 * i0, 2 * n, x);
-      load8(src, F32, si + 2 * i0 + 8, 2 * n - 8, y);
-      auto turn = [&](float (&v)[8], int j0) {
+  for (int u0 = threadIdx.x; u0 < all; u0 += 2 * kRopeThreads) {
+    if (u0 != (int)threadIdx.x) fetch(u0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 r = j0 + j < n ? a[j0 + j] : make_float2(0.0f, 0.0f);
-          const float v0 = v[2 * j], v1 = v[2 * j + 1];
-          v[2 * j] = v0 * r.x - v1 * r.y;
-          v[2 * j + 1] = v1 * r.x + v0 * r.y;
+    for (int q = 0; q < 2; ++q) {
+      if (w[q] < pu) {
+        const float2* a = cs + tk[q] * np;
+        if (halves) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 r = a[min(8 * w[q] + j, np - 1)];
+            const float v0 = x[q][j], v1 = y[q][j];
+            x[q][j] = v0 * r.x - v1 * r.y;
+            y[q][j] = v1 * r.x + v0 * r.y;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 r = a[min(4 * w[q] + j, np - 1)], r2 = a[min(4 * (w[q] + pu) + j, np - 1)];
+            const float v0 = x[q][2 * j], v1 = x[q][2 * j + 1], v2 = y[q][2 * j], v3 = y[q][2 * j + 1];
+            x[q][2 * j] = v0 * r.x - v1 * r.y;
+            x[q][2 * j + 1] = v1 * r.x + v0 * r.y;
+            y[q][2 * j] = v2 * r2.x - v3 * r2.y;
+            y[q][2 * j + 1] = v3 * r2.x + v2 * r2.y;
+          }
         }
-      };
-      turn(x, 0);
-      turn(y, 4);
-      store8(dst, F32, di + 2 * i0, 2 * n, x);
-      store8(dst, F32, di + 2 * i0 + 8, 2 * n - 8, y);
-    } else {
-      load8(src, F32, si + i0, n, x);
-      load8(src, F32, si + np + i0, n, y);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 r = j < n ? a[j] : make_float2(0.0f, 0.0f);
-        const float v0 = x[j], v1 = y[j];
-        x[j] = v0 * r.x - v1 * r.y;
-        y[j] = v1 * r.x + v0 * r.y;
       }
-      store8(dst, F32, di + i0, n, x);
-      store8(dst, F32, di + np + i0, n, y);
+      store8(dst[q], F32, 0, n[q], x[q]);
+      store8(dst[q], F32, second[q], n2[q], y[q]);
     }
   }
 }
@@ -144,8 +156,13 @@ hipError_t launch_rope(RopeParams p, hipStream_t s) {
   tw = tw < 1 ? 1 : (tw > 8 ? 8 : tw);
   const int64_t cu = device_cu_count();
   while (tw > 1 && (p.tokens + tw - 1) / tw < 2 * cu) tw >>= 1;
-  const int64_t tb = (p.tokens + tw - 1) / tw;
+  const int64_t units = (p.interleaved ? (2 * p.pairs + 15) / 16 : (p.pairs + 7) / 8) +
+                        (p.copy_rest ? (p.dim - 2 * p.pairs + 15) / 16 : 0);
+  if (units == 0) return hipSuccess;   // no pair and nothing to copy
   int64_t hw = heads < 256 ? heads : 256;
+  while (hw > 1 && tw * hw * units > 65535) hw = (hw + 1) / 2;   // units are divided in 16 bits
+  while (tw > 1 && tw * hw * units > 65535) tw >>= 1;
+  const int64_t tb = (p.tokens + tw - 1) / tw;
   while (hw > 8 && tb * ((heads + hw - 1) / hw) < 2 * cu) hw = (hw + 1) / 2;
   p.tokens_wg = (int)tw;
   p.heads_wg = (int)hw;
