@@ -135,8 +135,23 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
     }
   }
 
-  // the wavefronts' sums, each [16 MT][32], then 16 rows per wavefront
+  // the wavefronts' sums, each [16 MT][32], then 16 rows per wavefront, whose scales,
+  // bias and residual are on their way before the wavefronts meet
   float* mine = reinterpret_cast<float*>(lds + wave * SUMS);
+  uint32_t top = 0;
+  W w(p, e, n0, lane);
+  static_assert(W::RPL == 1, "a lane has one row of 8 columns");
+  const int r = 16 * wave + w.rg;
+  uint32_t o[1][W::SW];
+  float sa = 0.0f, sb[8] = {};
+  if (wave < MT) {
+    w.fetch(16 * wave, o);
+    if (!BLOCK && K > 0) {
+      sa = p.a_sinv[p.a_scaling == 5 ? min((int64_t)r, M - 1) : 0];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sb[k] = p.b_sinv[p.b_scaling == 5 ? min(w.c + k, N - 1) : 0];
+    }
+  }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -144,14 +159,8 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
       *reinterpret_cast<float4*>(mine + (16 * i + l16) * SK_COLS + 16 * j + 4 * g) =
           make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
   __syncthreads();
-  uint32_t top = 0;
   if (wave < MT) {
-    W w(p, e, n0, lane);
     uint8_t* wl = lds + SK_WAVES * SUMS + wave * EPB;
-    static_assert(W::RPL == 1, "a lane has one row of 8 columns");
-    const int r = 16 * wave + w.rg;
-    uint32_t o[1][W::SW];
-    w.fetch(16 * wave, o);
     float v[8] = {};
 #pragma unroll
     for (int s = 0; s < SK_WAVES; ++s) {
@@ -161,10 +170,8 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
       v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
     }
     if constexpr (!BLOCK) {
-      const float sa = K > 0 ? p.a_sinv[p.a_scaling == 5 ? min((int64_t)r, M - 1) : 0] : 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        v[k] = (v[k] * sa) * (K > 0 ? p.b_sinv[p.b_scaling == 5 ? min(w.c + k, N - 1) : 0] : 0.0f);
+      for (int k = 0; k < 8; ++k) v[k] = (v[k] * sa) * sb[k];
     }
     *w.place(wl, w.rg, 2 * w.cq) = make_float4(v[0], v[1], v[2], v[3]);
     *w.place(wl, w.rg, 2 * w.cq + 1) = make_float4(v[4], v[5], v[6], v[7]);
