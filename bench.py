@@ -780,8 +780,8 @@ def traffic_summarize(d, dst):
                 vals[int(r["Dispatch_Id"])][1] += float(r["Counter_Value"])
         return [vals[i] for i in sorted(vals)]
 
-    def nospace(t):
-        return re.sub(r"\s", "", t)
+    def nospace(t):   # (kernels without an epilogue carry its default type as their last argument)
+        return re.sub(r",[^,<>]*NoEpilogue", "", re.sub(r"\s", "", t))
 
     def classify(rows):
         """(copy values, {class: [values]}): the launches in traffic_run's

@@ -44,47 +44,45 @@ __device__ __forceinline__ void activate(int act, float (&v)[8], const float (&u
   }
 }
 
-// Eight values of a row of bf16 or binary32, as they lie in memory (see Raw8 in
-// op_device.h); n: how many there are.
-template <bool FAST, int W>
-__device__ __forceinline__ void load_packed(const void* p, int f32, int n, uint32_t (&w)[W]) {
+// Eight values of a row of bf16 or binary32 (WIDE: may be), as they lie in memory
+// (see Raw8 in op_device.h); n: how many there are.  Words: a vector where several
+// strips' are kept (arrays of arrays went to scratch memory), an array otherwise.  The
+// first 16 bytes are loaded ahead of the choice of type: loads of the same words in two
+// branches wait where the branches meet, 15% of a whole product's time.
+typedef uint32_t v8u __attribute__((ext_vector_type(8)));
+
+template <bool FAST, bool WIDE, typename Words>
+__device__ __forceinline__ void load_packed(const void* p, int f32, int n, Words& w) {
   if (n <= 0) return;
-  if constexpr (FAST) {
-    const Pk16a4 a = *reinterpret_cast<const Pk16a4*>(p);
+  const bool wide = WIDE && f32;
+  if (FAST || n >= 8) {
+    const uint32_t odd = FAST ? 0u : odd_of(p);
+    const Pk16a4 a = *reinterpret_cast<const Pk16a4*>(reinterpret_cast<const char*>(p) - odd);
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = a.v[k];
-    if constexpr (W == 8) {
-      if (f32) {
+    if constexpr (WIDE) {
+      if (wide) {
         const Pk16a4 b = *(reinterpret_cast<const Pk16a4*>(p) + 1);
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k + 4] = b.v[k];
+        return;
       }
+    }
+    if constexpr (!FAST) {
+      w[4] = 0u;
+      if (odd) w[4] = reinterpret_cast<const uint16_t*>(p)[7];
     }
     return;
-  } else {
-  if constexpr (W == 8) {
-    if (f32) {
+  }
+  if constexpr (!FAST) {
+    if (wide) {
       const float* q = reinterpret_cast<const float*>(p);
-      if (n >= 8) {
-        const Pk16a4 a = *reinterpret_cast<const Pk16a4*>(q);
-        const Pk16a4 b = *reinterpret_cast<const Pk16a4*>(q + 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          w[k] = a.v[k];
-          w[k + 4] = b.v[k];
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = k < n ? __float_as_uint(q[k]) : 0u;
-      }
+      for (int k = 0; k < 8; ++k) w[k] = k < n ? __float_as_uint(q[k]) : 0u;
       return;
     }
-  }
-  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-  uint32_t d[5] = {0u, 0u, 0u, 0u, 0u};
-  if (n >= 8) {
-    load_dwords(q, d);
-  } else {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    uint32_t d[5] = {0u, 0u, 0u, 0u, 0u};
 #pragma unroll
     for (int k = 0; k < 7; ++k)
       if (k < n) d[k >> 1] |= (uint32_t)q[k] << (16 * (k & 1));
@@ -93,9 +91,8 @@ __device__ __forceinline__ void load_packed(const void* p, int f32, int n, uint3
       for (int k = 4; k >= 1; --k) d[k] = __builtin_amdgcn_alignbyte(d[k], d[k - 1], 2);
       d[0] <<= 16;
     }
-  }
 #pragma unroll
-  for (int k = 0; k < 5; ++k) w[k] = d[k];
+    for (int k = 0; k < 5; ++k) w[k] = d[k];
   }
 }
 
@@ -190,8 +187,9 @@ struct EpWave {
   static constexpr int LPR = WTN / 8;        // lanes per row
   static constexpr int RPL = WTN / 32;       // rows per lane and strip of 16
   static_assert(RPL == 1 || RPL == 2 || RPL == 4, "32, 64 or 128 columns");
+  static constexpr bool WIDE = !OUT8 && DIR != EP_BWD;   // src may be binary32
+  using Words = typename std::conditional<FAST, uint32_t[WIDE ? 8 : 4], v8u>::type;
   static constexpr int CH = WTN / 4;         // 16-byte chunks of a strip's row
-  static constexpr int SW = OUT8 ? (FAST ? 4 : 5) : 8;   // words of eight values of src in flight
   const GemmParams& p;
   const EpParams& e;
   int lane, cq, rg, nv;
@@ -222,24 +220,24 @@ struct EpWave {
 
   // The strip of rows m0 .. m0 + 15 of src, in flight until stage() puts it into
   // LDS, where the loop over the rows can index it.
-  __device__ __forceinline__ void fetch(int64_t m0, uint32_t (&o)[RPL][SW]) {
+  __device__ __forceinline__ void fetch(int64_t m0, Words (&o)[RPL]) {
     if (src == nullptr) return;
 #pragma unroll
     for (int t = 0; t < RPL; ++t) {
       const int64_t m = m0 + rg * RPL + t;
-      load_packed<FAST>(src + m * src_ld, src_f32, m < p.M ? nv : 0, o[t]);
+      load_packed<FAST, WIDE>(src + m * src_ld, src_f32, m < p.M ? nv : 0, o[t]);
     }
   }
   // Each lane's own words: 16 bytes per lane and row for bf16, twice that for
   // binary32.
   static constexpr int SRC_BYTES = RPL * 64 * 16;
-  __device__ __forceinline__ void stage(int64_t m0, const uint32_t (&o)[RPL][SW], uint8_t* ol) {
+  __device__ __forceinline__ void stage(int64_t m0, const Words (&o)[RPL], uint8_t* ol) {
     if (src == nullptr) return;
     uint4* q = reinterpret_cast<uint4*>(ol) + lane;
 #pragma unroll
     for (int t = 0; t < RPL; ++t) {
       if (FAST || src_f32) q[t * 64] = make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
-      if constexpr (!OUT8) {
+      if constexpr (WIDE) {
         if (src_f32) q[(RPL + t) * 64] = make_uint4(o[t][4], o[t][5], o[t][6], o[t][7]);
       }
       if constexpr (!FAST) {
@@ -270,7 +268,7 @@ struct EpWave {
     char* aux = (!backward() && e.aux)
                     ? reinterpret_cast<char*>(const_cast<void*>(e.aux)) + (first * e.ldaux + c) * 2 : nullptr;
     const uint4* q = reinterpret_cast<const uint4*>(ol) + lane;
-    const bool wide = !OUT8 && src != nullptr && src_f32;
+    const bool wide = WIDE && src != nullptr && src_f32;
 #pragma unroll 1
     for (int t = 0; t < RPL; ++t) {
       const float4 w0 = *place(wl, rg * RPL + t, 2 * cq), w1 = *place(wl, rg * RPL + t, 2 * cq + 1);
@@ -351,22 +349,29 @@ struct EpWave {
   static constexpr int bytes(int TI) { return codes_at + (OUT8 ? WTN * (16 * TI + 16) : 0); }
 
   // Accumulators to strips.  acc[i][j] of lane (g, l16): row r0 + 16 i + l16,
-  // columns n0 + 16 j + 4 g .. + 3.  wl: bytes(TI) of LDS, wavefront-private.
+  // columns n0 + 16 j + 4 g .. + 3.  wl: bytes(TI) of LDS, wavefront-private.  Here src
+  // is fetched strip by strip; below (o) every strip's words are there already.
   template <int TI, int TJ, typename Deq>
   __device__ __forceinline__ void tile(const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t n0, uint8_t* wl) {
+    Words o[1][RPL];
+    fetch(r0, o[0]);
+    tile(acc, deq, r0, n0, wl, o);
+  }
+  template <int TI, int TJ, int STRIPS, typename Deq>
+  __device__ __forceinline__ void tile(const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t n0, uint8_t* wl,
+                                       Words (&o)[STRIPS][RPL]) {
     static_assert(16 * TJ == WTN, "the wavefront's columns");
+    static_assert(STRIPS == 1 || STRIPS == TI, "one strip ahead, or all");
     constexpr int TS = 16 * TI + 16;
     const int g = lane >> 4, l16 = lane & 15;
-    uint32_t o[RPL][SW];
-    fetch(r0, o);
     ep_for<0, TI>([&](auto itag) {
       constexpr int i = decltype(itag)::value;
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
         *place(wl, l16, 4 * j + g) = make_float4(deq(i, j, 0, acc[i][j][0]), deq(i, j, 1, acc[i][j][1]),
                                                  deq(i, j, 2, acc[i][j][2]), deq(i, j, 3, acc[i][j][3]));
-      stage(r0 + 16 * i, o, wl + src_at);
-      if constexpr (i + 1 < TI) fetch(r0 + 16 * (i + 1), o);
+      stage(r0 + 16 * i, o[STRIPS == 1 ? 0 : i], wl + src_at);
+      if constexpr (STRIPS == 1 && i + 1 < TI) fetch(r0 + 16 * (i + 1), o[0]);
       rows<TS>(r0 + 16 * i, wl, wl + src_at, wl + codes_at, 16 * i);
     });
     if constexpr (OUT8) {

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
   W w(p, e, n0, lane);
   static_assert(W::RPL == 1, "a lane has one row of 8 columns");
   const int r = 16 * wave + w.rg;
-  uint32_t o[1][W::SW];
+  typename W::Words o[1];
   float sa = 0.0f, sb[8] = {};
   if (wave < MT) {
     w.fetch(16 * wave, o);

@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(256) k_ep_join(GemmParams p, EpParams e) {
   const int64_t n0 = (int64_t)blockIdx.x * 128 + 32 * wave, m0 = (int64_t)blockIdx.y * 16;
   uint8_t* wl = lds + wave * BYTES;
   W w(p, e, n0, lane);
-  uint32_t o[1][W::SW];
+  typename W::Words o[1];
   w.fetch(m0, o);
   const int64_t m = m0 + w.rg;
   float v[8] = {};
