@@ -1,8 +1,13 @@
 // gemm_ep_large.h -- the large-tile kernels (k_gemm_w4, k_gemm_big) with the
 // linear's epilogue, for the operands a layer's forward and dgrad products have:
-// B (the weights) in E4M3, A in E4M3 forward and E5M2 backward; per-tensor, per-row, or block scales with A in 1x128
-// segments and B in 128x128 blocks.  Everything else runs on the tile kernels
-// (gemm_ep_tile.h), which take any combination.
+// B (the weights) in E4M3, A in E4M3 forward and E5M2 backward; per-tensor, per-row,
+// or block scales with A in 1x128 segments and B in 128x128 blocks.  Everything else
+// runs on the tile kernels (gemm_ep_tile.h), which take any combination.
+//
+// Bound: the matrix units, as without the epilogue.  Measured on an MI355X: 8192 x
+// 28672 x 8192, GELU, stored pre-activation, FP8 out with transposed copy, 1.60 ms,
+// 2.40 PFLOP/s (fp8_scaled_gemm at 8192^3: 2.52); backward 8192 x 14336 x 4096 with 1x128
+// scales and bias gradient 516 us, 1.86 PFLOP/s, where the promotion bounds it.
 #pragma once
 
 #include "gemm_w4_kernel.h"

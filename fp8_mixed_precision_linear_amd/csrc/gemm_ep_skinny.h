@@ -1,5 +1,5 @@
 // gemm_ep_skinny.h -- the FP8 product with the linear's epilogue for few rows of
-// A (one token up to 64), where the weights' bytes are the work; instantiated by
+// A (up to 16), where the weights' bytes are the work; instantiated by
 // gemm_ep_skinny.hip and gemm_ep_skinny_fp8out.hip.
 //
 // A workgroup owns 32 columns; its eight wavefronts take every eighth 128-byte
@@ -9,10 +9,14 @@
 // fragments (from L2: A is small and shared) take the same bytes of K.  U steps are in flight per wavefront, each
 // reloaded as soon as its products are issued, so a compute unit keeps
 // 8 U 4 KB = 128 KB of weights under way; there is no barrier until the end, where
-// the wavefronts' sums are added in order through LDS and MT wavefronts apply the
-// epilogue to 16 rows each.  No part of K goes to another workgroup: even 32
+// the wavefronts' sums are added in order through LDS and one wavefront applies the
+// epilogue.  No part of K goes to another workgroup: even 32
 // workgroups (1024 columns) can draw more than memory gives, and the join of
 // parts through memory would be a second launch.
+//
+// Bound: HBM.  Measured on an MI355X, per-row scales, bias and residual: one token,
+// 8192 x 8192, 18.4 us, 3.6 TB/s; 28672 x 8192 53 us, 4.4 TB/s; 16 tokens, 8192 x
+// 8192, 19.9 us.
 #pragma once
 
 #include "gemm_big_kernel.h"
@@ -30,33 +34,30 @@ __device__ __forceinline__ const float* scale_ptr(int scaling, const float* s, i
   return s + (scaling == 0 ? 0 : (scaling == 1 ? row : row / 128));
 }
 
-// MT: tiles of 16 rows.  BLOCK: block scales, promoted into binary32 per step;
+// BLOCK: block scales, promoted into binary32 per step;
 // SBCOL: B's differ by column (1x128 segments), else one per step.
-template <int AF, int BF, bool BLOCK, bool SBCOL, bool OUT8, int MT>
+template <int AF, int BF, bool BLOCK, bool SBCOL, bool OUT8>
 __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpParams e) {
-  constexpr int NT = SK_COLS / 16, U = MT == 4 ? 2 : 4;
+  constexpr int NT = SK_COLS / 16, U = 4;
   using W = EpWave<SK_COLS, OUT8, EP_ANY, false>;
-  constexpr int TS = 32, EPB = W::bytes(1), SUMS = 16 * MT * SK_COLS * 4;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[SK_WAVES * SUMS + MT * EPB];
+  constexpr int TS = 32, EPB = W::bytes(1), SUMS = 16 * SK_COLS * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[SK_WAVES * SUMS + EPB];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, l16 = lane & 15;
   const int64_t M = p.M, N = p.N, n0 = (int64_t)blockIdx.x * SK_COLS;
   const int nk = (int)((p.K + BK - 1) / BK), K = (int)p.K;
 
-  const uint8_t* arow[MT];
+  const uint8_t* arow = p.A + min((int64_t)l16, M - 1) * p.lda + 16 * g;
   const uint8_t* brow[NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) arow[i] = p.A + min((int64_t)(16 * i + l16), M - 1) * p.lda + 16 * g;
 #pragma unroll
   for (int j = 0; j < NT; ++j) brow[j] = p.B + min(n0 + 16 * j + l16, N - 1) * p.ldb + 16 * g;
   // block scales: A's of this lane's row, B's of its 4 columns or of the block
-  const float* asc[MT];
+  const float* asc = nullptr;
   const float* bsc[NT][SBCOL ? 4 : 1];
   int64_t astep = 0, bstep = 0;
   if constexpr (BLOCK) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i) asc[i] = scale_ptr(p.a_scaling, p.a_sinv, M, min((int64_t)(16 * i + l16), M - 1), astep);
+    asc = scale_ptr(p.a_scaling, p.a_sinv, M, min((int64_t)l16, M - 1), astep);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -65,8 +66,8 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
   }
 
   struct Step {
-    v8i a[MT], b[NT];
-    float sa[BLOCK ? MT : 1], sb[BLOCK ? NT : 1][SBCOL ? 4 : 1];
+    v8i a, b[NT];
+    float sa, sb[BLOCK ? NT : 1][SBCOL ? 4 : 1];
   };
   auto line = [&](const uint8_t* row, int k) -> v8i {   // zeros past K (a multiple of 16)
     uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
@@ -83,42 +84,34 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
     if (k + BK <= K) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) s.b[j] = whole(brow[j], k);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) s.a[i] = whole(arow[i], k);
+      s.a = whole(arow, k);
     } else {
 #pragma unroll
       for (int j = 0; j < NT; ++j) s.b[j] = line(brow[j], k);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) s.a[i] = line(arow[i], k);
+      s.a = line(arow, k);
     }
     if constexpr (BLOCK) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) s.sa[i] = asc[i][kb * astep];
+      s.sa = asc[kb * astep];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int q = 0; q < (SBCOL ? 4 : 1); ++q) s.sb[j][q] = bsc[j][q][kb * bstep];
     }
   };
-  v4f acc[MT][NT];
+  v4f acc[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < NT; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
   auto use = [&](const Step& s) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < NT; ++j) {
+      if constexpr (BLOCK) {
+        const v4f part = mfma<BF, AF>(s.b[j], s.a, v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if constexpr (BLOCK) {
-          const v4f part = mfma<BF, AF>(s.b[j], s.a[i], v4f{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            acc[i][j][q] = __builtin_fmaf(part[q] * s.sa[i], s.sb[j][SBCOL ? q : 0], acc[i][j][q]);
-        } else {
-          acc[i][j] = mfma<BF, AF>(s.b[j], s.a[i], acc[i][j]);
-        }
+        for (int q = 0; q < 4; ++q) acc[j][q] = __builtin_fmaf(part[q] * s.sa, s.sb[j][SBCOL ? q : 0], acc[j][q]);
+      } else {
+        acc[j] = mfma<BF, AF>(s.b[j], s.a, acc[j]);
       }
+    }
   };
   Step ring[U];
 #pragma unroll
@@ -135,17 +128,17 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
     }
   }
 
-  // the wavefronts' sums, each [16 MT][32], then 16 rows per wavefront, whose scales,
-  // bias and residual are on their way before the wavefronts meet
+  // the wavefronts' sums, each [16][32], then the rows' epilogue by the first, whose
+  // scales, bias and residual are on their way before the wavefronts meet
   float* mine = reinterpret_cast<float*>(lds + wave * SUMS);
   uint32_t top = 0;
   W w(p, e, n0, lane);
   static_assert(W::RPL == 1, "a lane has one row of 8 columns");
-  const int r = 16 * wave + w.rg;
+  const int r = w.rg;
   typename W::Words o[1];
   float sa = 0.0f, sb[8] = {};
-  if (wave < MT) {
-    w.fetch(16 * wave, o);
+  if (wave == 0) {
+    w.fetch(0, o);
     if (!BLOCK && K > 0) {
       sa = p.a_sinv[p.a_scaling == 5 ? min((int64_t)r, M - 1) : 0];
 #pragma unroll
@@ -153,14 +146,12 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
     }
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      *reinterpret_cast<float4*>(mine + (16 * i + l16) * SK_COLS + 16 * j + 4 * g) =
-          make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+  for (int j = 0; j < NT; ++j)
+    *reinterpret_cast<float4*>(mine + l16 * SK_COLS + 16 * j + 4 * g) =
+        make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
   __syncthreads();
-  if (wave < MT) {
-    uint8_t* wl = lds + SK_WAVES * SUMS + wave * EPB;
+  if (wave == 0) {
+    uint8_t* wl = lds + SK_WAVES * SUMS;
     float v[8] = {};
 #pragma unroll
     for (int s = 0; s < SK_WAVES; ++s) {
@@ -175,31 +166,25 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
     }
     *w.place(wl, w.rg, 2 * w.cq) = make_float4(v[0], v[1], v[2], v[3]);
     *w.place(wl, w.rg, 2 * w.cq + 1) = make_float4(v[4], v[5], v[6], v[7]);
-    w.stage(16 * wave, o, wl + W::src_at);
-    w.template rows<TS>(16 * wave, wl, wl + W::src_at, wl + W::codes_at, 0);
+    w.stage(0, o, wl + W::src_at);
+    w.template rows<TS>(0, wl, wl + W::src_at, wl + W::codes_at, 0);
     if constexpr (OUT8) {
-      if (p.D_t) w.template flush_t<TS, 16>(wl + W::codes_at, 16 * wave, n0);
+      if (p.D_t) w.template flush_t<TS, 16>(wl + W::codes_at, 0, n0);
     }
-    w.put_dbias(wave);
+    w.put_dbias(0);
     top = w.amax_bits();
   }
   if (p.d_amax) ep_amax<SK_WAVES>(p.d_amax, top, lane, wave);
 }
 
-template <int AF, int BF, bool OUT8, int MT>
-hipError_t launch_skinny_k(const GemmParams& p, const EpParams& e, hipStream_t s) {
-  const dim3 grid((unsigned)((p.N + SK_COLS - 1) / SK_COLS)), block(SK_WAVES * 64);
-  const bool blk = !((p.a_scaling == 0 || p.a_scaling == 5) && (p.b_scaling == 0 || p.b_scaling == 5));
-  if (!blk) hipLaunchKernelGGL((k_ep_skinny<AF, BF, false, false, OUT8, MT>), grid, block, 0, s, p, e);
-  else if (p.b_scaling == 1) hipLaunchKernelGGL((k_ep_skinny<AF, BF, true, true, OUT8, MT>), grid, block, 0, s, p, e);
-  else hipLaunchKernelGGL((k_ep_skinny<AF, BF, true, false, OUT8, MT>), grid, block, 0, s, p, e);
-  return hipGetLastError();
-}
 template <int AF, int BF, bool OUT8>
 hipError_t launch_skinny_f(const GemmParams& p, const EpParams& e, hipStream_t s) {
-  if (p.M <= 16) return launch_skinny_k<AF, BF, OUT8, 1>(p, e, s);
-  if (p.M <= 32) return launch_skinny_k<AF, BF, OUT8, 2>(p, e, s);
-  return launch_skinny_k<AF, BF, OUT8, 4>(p, e, s);
+  const dim3 grid((unsigned)((p.N + SK_COLS - 1) / SK_COLS)), block(SK_WAVES * 64);
+  const bool blk = !((p.a_scaling == 0 || p.a_scaling == 5) && (p.b_scaling == 0 || p.b_scaling == 5));
+  if (!blk) hipLaunchKernelGGL((k_ep_skinny<AF, BF, false, false, OUT8>), grid, block, 0, s, p, e);
+  else if (p.b_scaling == 1) hipLaunchKernelGGL((k_ep_skinny<AF, BF, true, true, OUT8>), grid, block, 0, s, p, e);
+  else hipLaunchKernelGGL((k_ep_skinny<AF, BF, true, false, OUT8>), grid, block, 0, s, p, e);
+  return hipGetLastError();
 }
 template <bool OUT8>
 hipError_t launch_skinny_out(const GemmParams& p, const EpParams& e, hipStream_t s) {

@@ -16,6 +16,12 @@
 // into the matrix instruction (EP_MX); others promote each step's product into the
 // binary32 accumulator, by the row's scale times the tile's one scale of B (EP_BLK:
 // B's columns lie in one 128 x 128 block) or each column's (EP_BLKCOL).
+//
+// Bound: the latency of a step between its barriers (0.44 us at 64 rows and one
+// workgroup per compute unit, of which the products are 0.12).  Measured on an MI355X:
+// 300 x 14336 x 4096 with SiLU and pre-activation 32.9 us, 1.07 PFLOP/s; 256 x 8192 x
+// 8192 per-tensor 35 us, power-of-two scales 41, promoted 40; backward 1037 x 1999 x
+// 2304 24 us, of which the bias gradient's join is 4.
 #pragma once
 
 #include "gemm_big_kernel.h"

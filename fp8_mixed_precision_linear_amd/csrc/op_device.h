@@ -15,7 +15,6 @@ namespace {
 // but the lines it straddles.
 struct __attribute__((packed, aligned(2))) Pk16a2 { uint32_t v[4]; };
 struct __attribute__((packed, aligned(4))) Pk16a4 { uint32_t v[4]; };
-struct __attribute__((packed, aligned(1))) Pk8a1 { uint32_t v[2]; };
 
 typedef float f32x2_op __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_op __attribute__((ext_vector_type(2)));
@@ -197,21 +196,6 @@ __device__ __forceinline__ void unpack(const Raw8<F32>& r, const void* row, cons
       v[2 * k] = bf16_lo(d);
       v[2 * k + 1] = bf16_hi(d);
     }
-  }
-}
-
-// Eight FP8 codes (two dwords) to element i of a byte array.
-__device__ __forceinline__ void store8_codes(uint8_t* base, int64_t i, int n, uint32_t lo, uint32_t hi) {
-  uint8_t* p = base + i;
-  if (n >= 8) {
-    Pk8a1 a;
-    a.v[0] = lo;
-    a.v[1] = hi;
-    *reinterpret_cast<Pk8a1*>(p) = a;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) p[k] = (uint8_t)((k < 4 ? lo : hi) >> (8 * (k & 3)));
   }
 }
 

@@ -13,7 +13,9 @@
 // into LDS, and read from there by all its heads.
 //
 // Bound: HBM, one read and one write of each head element; angles cost
-// rot / 2 per token however many heads turn by them.
+// rot / 2 per token however many heads turn by them.  Measured on an MI355X: 8192
+// tokens, 64 + 8 heads of 128, half of each turned, 69 us, 4.4 TB/s (a copy: 4.94);
+// 16 tokens 4.6 us of kernel.
 #include "op_device.h"
 #include "launch.h"
 
