@@ -32,7 +32,7 @@
 // Measured (MI355X, inputs that change from call to call; a copy of 2 x 2 GiB moves
 // 4.94 TB/s): 8192 x 8192 with channel gate and FP8 out 107 us, 4.4 TB/s; its gradient
 // 161 us, 5.0 TB/s, of which the join is 6; 1 x 8192 6.4 us of kernel; layer norm of
-// 1531 x 2053 in binary32 17.4 us, 2.5 TB/s; gradient of 777 x 4095 40 us, 1.4 TB/s,
+// 1531 x 2053 in binary32 17.4 us, 2.5 TB/s; gradient of 777 x 4095 33 us, 1.7 TB/s,
 // bound by its partial column sums.  Rows of an XCD kept contiguous: 5-8% slower.
 #include <atomic>
 
@@ -396,12 +396,16 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024)
 template <int VPT, bool ONE, bool LN, bool XF32, bool EACH, bool TINY>
 __global__ void __launch_bounds__(ONE ? 512 : 1024) k_norm_bwd(NormGradParams p, int G, int rpw) {
   constexpr int NA = LN ? 4 : 2;
-  constexpr bool AHEAD = ahead(ONE, VPT);
+  // The widest rows (binary32, four sums, a gate's values) have no registers left for
+  // the next row's loads: 8192 x 4096 155 us with them, 150 without; in bf16 112
+  // against 123.
+  constexpr bool AHEAD = ahead(ONE, VPT) && !(EACH && LN && XF32);
   __shared__ float4 red[ONE ? 1 : 2 * kMaxWaves];
   // The column sums, NA VPT vectors of 8 per thread, live in registers, or, where
-  // they would spill (the layer norm's four, or several vectors per thread), the
-  // first four of them in LDS: each thread its own words, 128 KB.
-  constexpr int SLOTS = !ONE && NA * VPT >= 4 ? 4 : 0;
+  // they would spill (the layer norm's four, several vectors per thread, or a gate's
+  // values beside them: 8192 x 4096 in binary32 with a gate per token 140 us so, 133
+  // as here), the first four of them in LDS: each thread its own words, up to 128 KB.
+  constexpr int SLOTS = ONE ? 0 : NA * VPT >= 4 ? 4 : EACH ? NA * VPT : 0;
   __shared__ __attribute__((aligned(16))) float sums[(SLOTS ? SLOTS : 1) * 8 * 1024];
   const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / G), t = (int)threadIdx.x - sub * G;
   Row<ONE> rs(red, G >> 6, (sub * G) >> 6);
@@ -552,20 +556,27 @@ __global__ void __launch_bounds__(ONE ? 512 : 1024) k_norm_bwd(NormGradParams p,
         d[i][k] = k >= c.x[i].skip ? d[i][k] : 0.0f;
       }
       if constexpr (EACH) {
-        float g[8], b[8], dg[8];
+        // (bias and gate one after the other: both in flight, this spilled twice the
+        // registers, and layer norm of 8192 x 4096 in binary32 took 177 us, now 155)
+        float g[8], dg[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) { g[k] = gt; b[k] = 0.0f; }
+        for (int k = 0; k < 8; ++k) dg[k] = 0.0f;
+        if (LN && p.b_post) load_vec<TINY>(p.b_post, p.p_f32, c.x[i], dg);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          dg[k] = d[i][k] * __builtin_fmaf(zh[k], w[k], dg[k]);
+          q[EACH ? 2 : 0] += dg[k];
+          g[k] = gt;
+        }
+        __builtin_amdgcn_sched_barrier(0);
         if (p.gate_kind == 3) {
           if (live) load_vec<TINY>(row_of(p.gate, row, p.ldg, 0), 0, c.x[i], g);
 #pragma unroll
           for (int k = 0; k < 8; ++k) g[k] = gate_value(p.gate_act, g[k]);
         }
-        if (LN && p.b_post) load_vec<TINY>(p.b_post, p.p_f32, c.x[i], b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float dn = d[i][k] * __builtin_fmaf(zh[k], w[k], b[k]);
-          q[EACH ? 2 : 0] += dn;
-          dg[k] = p.branch_scale * dn * gate_slope(p.gate_act, g[k]);
+          dg[k] = p.branch_scale * dg[k] * gate_slope(p.gate_act, g[k]);
           d[i][k] *= g[k];
         }
         if (p.dgate && p.gate_kind == 3) store_vec<TINY>(row_of(p.dgate, row, p.lddg, 0), 0, c.x[i], live, dg);
