@@ -214,10 +214,10 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
   }
   __syncthreads();   // the stages are free for the epilogue, rs_tab is written
 
-  float ta = 1.0f, tb = 1.0f;   // EP_MX: a per-tensor operand's scale
+  float ta = 1.0f, tb = 1.0f;   // EP_MX: a per-tensor operand's scale (without K there may be none)
   if constexpr (MODE == EP_MX) {
-    if (p.a_scaling == 0) ta = p.a_sinv[0];
-    if (p.b_scaling == 0) tb = p.b_sinv[0];
+    if (p.a_scaling == 0 && K > 0) ta = p.a_sinv[0];
+    if (p.b_scaling == 0 && K > 0) tb = p.b_sinv[0];
   }
   auto deq = [&](int i, int j, int q, float x) -> float {
     if constexpr (MODE == EP_BLK || MODE == EP_BLKCOL) return x;
