@@ -83,7 +83,7 @@ fp8_status fp8_block_norm(const fp8_norm_args* args, hipStream_t stream) {
 }
 
 int64_t fp8_block_norm_bwd_workspace(int64_t rows, int64_t cols) {
-  if (rows < 0 || cols <= 0) return 0;
+  if (rows < 0 || cols <= 0 || cols > norm_max_cols()) return 0;   // (the call refuses wider rows)
   return 4 * norm_parts(rows, cols) * cols * (int64_t)sizeof(float);
 }
 

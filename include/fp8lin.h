@@ -552,7 +552,8 @@ fp8_status fp8_block_norm(const fp8_norm_args* args, hipStream_t stream);
  *            for FP8_GATE_FULL);  dw_pre, db_pre, dw_post, db_post [cols],
  *            param_dtype: overwritten.
  *   Each output is optional.  rows == 0 sets the column sums to 0.
- *   workspace  fp8_block_norm_bwd_workspace(rows, cols) bytes.
+ *   workspace  fp8_block_norm_bwd_workspace(rows, cols) bytes (0 for sizes
+ *            that the call refuses).
  * Errors: as fp8_block_norm; FP8_ERR_NULL also for the workspace,
  * FP8_ERR_SHAPE for one that is too small, FP8_ERR_ARG for an output whose
  * input is missing.
