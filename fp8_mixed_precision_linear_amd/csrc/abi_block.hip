@@ -38,6 +38,36 @@ fp8_status norm_common(const A& a) {
   return FP8_OK;
 }
 
+// Checks a product's and its epilogue's arguments, all but the workspace, and, if
+// they are right, fills p and e.
+fp8_status ep_params(const fp8_gemm_args* a, const fp8_epilogue_args* ep, GemmParams& p, EpParams& e) {
+  if (a == nullptr || ep == nullptr) return FP8_ERR_NULL;
+  const fp8_status st = gemm_params(a, p);
+  if (st != FP8_OK) return st;
+  if (!flag_ok(ep->backward) || ep->act < FP8_ACT_NONE || ep->act > FP8_ACT_SILU) return FP8_ERR_ARG;
+  if (!dtype_ok(ep->param_dtype) || !dtype_ok(ep->residual_dtype)) return FP8_ERR_ARG;
+  if (ep->backward ? (ep->bias != nullptr || ep->residual != nullptr) : ep->dbias != nullptr) return FP8_ERR_ARG;
+  if (a->accumulate) return FP8_ERR_UNSUPPORTED;
+  if (p.d_fp8 && ep->residual != nullptr && ep->residual_dtype == FP8_DT_F32) return FP8_ERR_UNSUPPORTED;
+  if (a->M > 0 && a->N > 0) {
+    if (ep->backward && ep->act != FP8_ACT_NONE && ep->aux == nullptr) return FP8_ERR_NULL;
+    if (ep->aux != nullptr && ep->ldaux < a->N) return FP8_ERR_SHAPE;
+    if (ep->residual != nullptr && ep->ldres < a->N) return FP8_ERR_SHAPE;
+    if (a->K > 0 && !gemm_big_supported(p)) return FP8_ERR_UNSUPPORTED;
+    // the grid's threads are counted in 32 bits
+    if ((a->M + 127) / 128 > ((int64_t)1 << 23) / ((a->N + 127) / 128)) return FP8_ERR_UNSUPPORTED;
+  }
+  const unsigned ps = size_of(ep->param_dtype);
+  if (!aligned(ep->bias, ps) || !aligned(ep->dbias, ps) || !aligned(ep->aux, 2) ||
+      !aligned(ep->residual, size_of(ep->residual_dtype)) || !aligned(ep->workspace, 16))
+    return FP8_ERR_ALIGN;
+  e = {};
+  e.backward = ep->backward; e.act = ep->act; e.bias_f32 = ep->param_dtype; e.res_f32 = ep->residual_dtype;
+  e.bias = ep->bias; e.residual = ep->residual; e.ldres = ep->ldres; e.res_scale = ep->res_scale;
+  e.aux = ep->aux; e.ldaux = ep->ldaux; e.dbias = ep->dbias;
+  return FP8_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -141,36 +171,27 @@ int64_t fp8_scaled_gemm_ep_workspace(int64_t M, int64_t N, int64_t K, fp8_scalin
 }
 
 fp8_status fp8_scaled_gemm_ep(const fp8_gemm_args* gemm, const fp8_epilogue_args* ep, hipStream_t stream) {
-  if (gemm == nullptr || ep == nullptr) return FP8_ERR_NULL;
-  const fp8_gemm_args* a = gemm;
   GemmParams p;
-  const fp8_status st = gemm_params(a, p);
+  EpParams e;
+  const fp8_status st = ep_params(gemm, ep, p, e);
   if (st != FP8_OK) return st;
-  if (!flag_ok(ep->backward) || ep->act < FP8_ACT_NONE || ep->act > FP8_ACT_SILU) return FP8_ERR_ARG;
-  if (!dtype_ok(ep->param_dtype) || !dtype_ok(ep->residual_dtype)) return FP8_ERR_ARG;
-  if (ep->backward ? (ep->bias != nullptr || ep->residual != nullptr) : ep->dbias != nullptr) return FP8_ERR_ARG;
-  if (a->accumulate) return FP8_ERR_UNSUPPORTED;
-  if (p.d_fp8 && ep->residual != nullptr && ep->residual_dtype == FP8_DT_F32) return FP8_ERR_UNSUPPORTED;
-  if (a->M > 0 && a->N > 0) {
-    if (ep->backward && ep->act != FP8_ACT_NONE && ep->aux == nullptr) return FP8_ERR_NULL;
-    if (ep->aux != nullptr && ep->ldaux < a->N) return FP8_ERR_SHAPE;
-    if (ep->residual != nullptr && ep->ldres < a->N) return FP8_ERR_SHAPE;
-    if (a->K > 0 && !gemm_big_supported(p)) return FP8_ERR_UNSUPPORTED;
-    // the grid's threads are counted in 32 bits
-    if ((a->M + 127) / 128 > ((int64_t)1 << 23) / ((a->N + 127) / 128)) return FP8_ERR_UNSUPPORTED;
-  }
-  const unsigned ps = size_of(ep->param_dtype);
-  if (!aligned(ep->bias, ps) || !aligned(ep->dbias, ps) || !aligned(ep->aux, 2) ||
-      !aligned(ep->residual, size_of(ep->residual_dtype)) || !aligned(ep->workspace, 16))
-    return FP8_ERR_ALIGN;
-  const int64_t need = fp8_scaled_gemm_ep_workspace(a->M, a->N, a->K, a->a_scaling, a->b_scaling);
+  const int64_t need = fp8_scaled_gemm_ep_workspace(gemm->M, gemm->N, gemm->K, gemm->a_scaling, gemm->b_scaling);
   if (need > 0 && ep->workspace == nullptr) return FP8_ERR_NULL;
   if (ep->workspace_bytes < need) return FP8_ERR_SHAPE;
-  EpParams e = {};
-  e.backward = ep->backward; e.act = ep->act; e.bias_f32 = ep->param_dtype; e.res_f32 = ep->residual_dtype;
-  e.bias = ep->bias; e.residual = ep->residual; e.ldres = ep->ldres; e.res_scale = ep->res_scale;
-  e.aux = ep->aux; e.ldaux = ep->ldaux; e.dbias = ep->dbias;
   return launched(launch_gemm_ep(p, e, static_cast<uint8_t*>(ep->workspace), stream));
+}
+
+fp8_status fp8_scaled_gemm_ep_plan(const fp8_gemm_args* gemm, const fp8_epilogue_args* ep, fp8_ep_plan* plan) {
+  GemmParams p;
+  EpParams e;
+  const fp8_status st = ep_params(gemm, ep, p, e);
+  if (st != FP8_OK) return st;
+  if (plan == nullptr) return FP8_ERR_NULL;
+  const EpPlan t = ep_plan(p, e);
+  plan->kernel = t.large ? FP8_EP_LARGE : (t.skinny ? FP8_EP_FEW_ROWS : FP8_EP_TILES);
+  plan->tile_rows = t.large ? 256 : (t.skinny ? 16 : t.bm);
+  plan->k_parts = t.splits;
+  return FP8_OK;
 }
 
 fp8_status fp8_rope(const fp8_rope_args* args, hipStream_t stream) {

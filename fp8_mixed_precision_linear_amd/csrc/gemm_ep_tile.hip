@@ -148,6 +148,16 @@ bool large_takes(const GemmParams& p, const EpParams& e) {
 }
 }  // namespace
 
+EpPlan ep_plan(const GemmParams& p, const EpParams& e) {
+  EpPlan plan = ep_plan(p);
+  plan.large = plan.large && large_takes(p, e);
+  if (plan.large) {
+    plan.splits = 1;
+    plan.parts = plan.large_parts;
+  }
+  return plan;
+}
+
 hipError_t launch_gemm_ep_tile(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s) {
   return launch_tile_sum<false>(p, e, plan, s);
 }
@@ -159,24 +169,22 @@ hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStre
     if (err != hipSuccess) return err;
   }
   if (p.N == 0) return hipSuccess;
-  const EpPlan plan = ep_plan(p);
+  const EpPlan plan = ep_plan(p, e);
   e.part = reinterpret_cast<float*>(ws);
   e.sums = reinterpret_cast<float*>(ws + plan.part_bytes);
   e.ldw = plan.ldw;
-  const bool large = plan.large && large_takes(p, e);
-  e.splits = large ? 1 : plan.splits;
-  const int64_t parts = large ? plan.large_parts : plan.parts;
+  e.splits = plan.splits;
   // Power-of-two block scales on every block-scaled operand go into the matrix
   // instruction; beside others they are binary32 scales of the same layouts, as
   // they are for the few-row kernel (bound by memory, not by the promotion).
   const bool promoted = p.a_scaling == 1 || p.a_scaling == 2 || p.b_scaling == 1 || p.b_scaling == 2;
-  if (!large) {
+  if (!plan.large) {
     if (p.a_scaling == 3 || p.a_scaling == 4) p.a_scaling -= 2;
     if (p.b_scaling == 3 || p.b_scaling == 4) p.b_scaling -= 2;
   }
   if (p.M > 0) {
     hipError_t err;
-    if (large) err = p.d_fp8 ? launch_gemm_ep_large_fp8out(p, e, s) : launch_gemm_ep_large(p, e, s);
+    if (plan.large) err = p.d_fp8 ? launch_gemm_ep_large_fp8out(p, e, s) : launch_gemm_ep_large(p, e, s);
     else if (plan.skinny) err = p.d_fp8 ? launch_gemm_ep_skinny_fp8out(p, e, s) : launch_gemm_ep_skinny(p, e, s);
     else if (promoted) err = p.d_fp8 ? launch_gemm_ep_tile_blk_fp8out(p, e, plan, s) : launch_gemm_ep_tile_blk(p, e, plan, s);
     else err = p.d_fp8 ? launch_gemm_ep_tile_fp8out(p, e, plan, s) : launch_gemm_ep_tile(p, e, plan, s);
@@ -190,7 +198,7 @@ hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStre
     }
   }
   if (e.dbias) {
-    hipLaunchKernelGGL(k_ep_dbias, dim3((unsigned)((p.N + 63) / 64)), dim3(1024), 0, s, e.part, parts, p.N,
+    hipLaunchKernelGGL(k_ep_dbias, dim3((unsigned)((p.N + 63) / 64)), dim3(1024), 0, s, e.part, plan.parts, p.N,
                        e.dbias, e.bias_f32);
     return hipGetLastError();
   }

@@ -200,10 +200,11 @@ struct EpPlan {
   int bm, bn, splits;
   bool large;   // 256 x 256 tiles of the large kernels
   bool skinny;  // few rows: weights streamed to registers
-  int64_t parts, large_parts;   // rows of column sums, off and on the large kernels
+  int64_t parts, large_parts;   // rows of column sums; on the large kernels
   int64_t ldw, part_bytes, sums_bytes;
 };
-EpPlan ep_plan(const GemmParams& p);
+EpPlan ep_plan(const GemmParams& p);                      // what the workspace has to allow for
+EpPlan ep_plan(const GemmParams& p, const EpParams& e);   // what a call takes
 // Power-of-two scalings keep their codes in launch_gemm_ep_large*, are block
 // scales like any others in the tile kernels.
 hipError_t launch_gemm_ep_large(const GemmParams& p, const EpParams& e, hipStream_t s);

@@ -29,6 +29,7 @@ NORM_RMS, NORM_LAYER = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 GATE_LINEAR, GATE_SIGMOID, GATE_TANH = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+EP_FEW_ROWS, EP_TILES, EP_LARGE = 0, 1, 2
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = 0, 1, 2, 3
 
@@ -91,6 +92,10 @@ class EpilogueArgs(C.Structure):
                 ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
 
 
+class EpPlan(C.Structure):
+    _fields_ = [("kernel", C.c_int), ("tile_rows", C.c_int), ("k_parts", C.c_int)]
+
+
 class RopeArgs(C.Structure):
     _fields_ = [("tokens", C.c_int64), ("q_heads", C.c_int64), ("k_heads", C.c_int64),
                 ("dim", C.c_int64), ("pairs", C.c_int64),
@@ -134,6 +139,7 @@ def _load():
         "fp8_block_norm_bwd": (i32, [vp, vp]),
         "fp8_scaled_gemm_ep_workspace": (i64, [i64, i64, i64, i32, i32]),
         "fp8_scaled_gemm_ep": (i32, [vp, vp, vp]),
+        "fp8_scaled_gemm_ep_plan": (i32, [vp, vp, vp]),
         "fp8_rope": (i32, [vp, vp]),
         "fp8_rope_freqs": (i32, [vp, i64, C.c_double, i32, C.c_double, C.c_double, C.c_double, C.c_double, vp]),
     }

@@ -628,6 +628,22 @@ int64_t fp8_scaled_gemm_ep_workspace(int64_t M, int64_t N, int64_t K, fp8_scalin
 fp8_status fp8_scaled_gemm_ep(const fp8_gemm_args* gemm, const fp8_epilogue_args* ep,
                               hipStream_t stream);
 
+/* fp8_scaled_gemm_ep_plan -- which kernel fp8_scaled_gemm_ep takes with these
+ * arguments on the current device (nothing is enqueued, no pointer is read; the
+ * workspace is not looked at): for tests and profiles, since the choice goes by
+ * measured times and may change.  Errors: as the call's; FP8_ERR_NULL (plan). */
+typedef enum {
+  FP8_EP_FEW_ROWS = 0,   /* up to 16 rows, weights streamed from memory */
+  FP8_EP_TILES = 1,      /* tiles of tile_rows x 128, K in k_parts parts */
+  FP8_EP_LARGE = 2       /* tiles of 256 x 256 */
+} fp8_ep_kernel;
+typedef struct {
+  fp8_ep_kernel kernel;
+  int tile_rows, k_parts;
+} fp8_ep_plan;
+
+fp8_status fp8_scaled_gemm_ep_plan(const fp8_gemm_args* gemm, const fp8_epilogue_args* ep, fp8_ep_plan* plan);
+
 /* ------------------------------------------------------------------------
  * fp8_rope -- rotary positions of the query and key heads of a QKV product.
  * Pair i < pairs of a head is (i, i + pairs) (FP8_ROPE_HALF) or (2i, 2i + 1)

@@ -28,3 +28,30 @@ def test_norm_gradient_wider_than_its_rows(L, rows, cols):
 def test_norm_gradient_workspace(L, rows, cols):
     n = L._L.fp8_block_norm_bwd_workspace(rows, cols)
     assert n > 0 and n % (16 * cols) == 0   # four rows of binary32 sums per workgroup
+
+
+def product(L, call, M=8, N=16, K=128, **kw):
+    g = L.GemmArgs(M=M, N=N, K=K, lda=kw.pop("lda", K), ldb=kw.pop("ldb", K), ldd=N, A=0x1000, a_fmt=0, a_scaling=0, a_scale_inv=0x2000,
+                   B=0x3000, b_fmt=0, b_scaling=0, b_scale_inv=0x4000, D=0x5000, d_dtype=0)
+    e = L.EpilogueArgs(backward=0, act=0, param_dtype=0, res_scale=1.0, workspace=0x10000, workspace_bytes=1 << 62)
+    for k, v in kw.items():
+        setattr(e if hasattr(e, k) else g, k, v)
+    return call(C.byref(g), C.byref(e))
+
+
+def test_product_plan(L):
+    plan = L.EpPlan()
+
+    def ask(g, e):
+        return L._L.fp8_scaled_gemm_ep_plan(g, e, C.byref(plan))
+
+    for size, want in [((1, 4096, 4096), (L.EP_FEW_ROWS, 16, 1)), ((16, 4096, 4096), (L.EP_FEW_ROWS, 16, 1)),
+                       ((8192, 8192, 8192), (L.EP_LARGE, 256, 1)), ((0, 64, 64), (L.EP_FEW_ROWS, 16, 1))]:
+        assert product(L, ask, *size) == 0 and (plan.kernel, plan.tile_rows, plan.k_parts) == want
+    assert product(L, ask, 8192, 8191, 8192) == 0 and plan.kernel == L.EP_TILES      # not for whole vectors
+    assert product(L, ask, 64, 512, 8192) == 0 and plan.kernel == L.EP_TILES and plan.k_parts > 1
+    # the workspace is not looked at; everything else is refused as by the call
+    assert product(L, ask, workspace=None, workspace_bytes=0) == 0
+    assert product(L, ask, K=100) == SHAPE and product(L, ask, act=9) == ARG and product(L, ask, aux=0x6001, ldaux=16) == ALIGN
+    assert product(L, lambda g, e: L._L.fp8_scaled_gemm_ep_plan(g, e, None)) == NULL
+    assert L._L.fp8_scaled_gemm_ep_plan(None, None, C.byref(plan)) == NULL
