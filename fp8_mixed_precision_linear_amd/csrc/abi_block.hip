@@ -54,8 +54,10 @@ fp8_status ep_params(const fp8_gemm_args* a, const fp8_epilogue_args* ep, GemmPa
     if (ep->aux != nullptr && ep->ldaux < a->N) return FP8_ERR_SHAPE;
     if (ep->residual != nullptr && ep->ldres < a->N) return FP8_ERR_SHAPE;
     if (a->K > 0 && !gemm_big_supported(p)) return FP8_ERR_UNSUPPORTED;
-    // the grid's threads are counted in 32 bits
+    // the grids' threads are counted in 32 bits: tiles of 128 x 128, the few-row
+    // kernel's 16 per column, the bias gradient's 16 per column
     if ((a->M + 127) / 128 > ((int64_t)1 << 23) / ((a->N + 127) / 128)) return FP8_ERR_UNSUPPORTED;
+    if (a->N > ((int64_t)1 << 28) - 64 && (a->M <= 16 || ep->dbias != nullptr)) return FP8_ERR_UNSUPPORTED;
   }
   const unsigned ps = size_of(ep->param_dtype);
   if (!aligned(ep->bias, ps) || !aligned(ep->dbias, ps) || !aligned(ep->aux, 2) ||

@@ -105,6 +105,7 @@ EpPlan ep_plan(const GemmParams& p) {
   const bool per_a = p.a_scaling == 0 || p.a_scaling == 5, per_b = p.b_scaling == 0 || p.b_scaling == 5;
   const bool layer = per_a ? per_b : p.a_scaling == 1 ? p.b_scaling == 2 : p.a_scaling == 3 ? p.b_scaling == 4 : false;
   const int64_t cu = device_cu_count(), nk = (p.K + BK - 1) / BK;
+  const bool parts = (p.M + 15) / 16 <= 65535;   // the join's grid: 16 rows per workgroup in y
   plan.skinny = p.M <= 16;
   plan.bm = 32;
   plan.bn = 128;
@@ -113,7 +114,7 @@ EpPlan ep_plan(const GemmParams& p) {
     const TileCost* cost = kCost[per_a && per_b ? 0 : 1];
     float best = 0.0f;
     for (int i = 0; i < 3; ++i)
-      for (int splits = 1; splits <= 16 && (splits == 1 || nk / splits >= 2); splits *= 2) {
+      for (int splits = 1; splits <= 16 && (splits == 1 || (parts && nk / splits >= 2)); splits *= 2) {
         const float t = tile_time(cost[i], p.M, p.N, nk, splits, cu);
         if (best != 0.0f && t >= best) continue;
         best = t;

@@ -605,8 +605,9 @@ fp8_status fp8_block_norm_bwd(const fp8_norm_bwd_args* args, hipStream_t stream)
  * dtypes, bias or residual in a backward call, dbias in a forward one),
  * FP8_ERR_NULL (aux of a backward call, workspace), FP8_ERR_SHAPE (ldaux,
  * ldres < N, a workspace that is too small), FP8_ERR_UNSUPPORTED (gemm's
- * accumulate; 256 * lda or 256 * ldb >= 2^31; an FP32 residual beside an FP8
- * output).
+ * accumulate; 256 * lda or 256 * ldb >= 2^31; K > 65536; more than 2^23 tiles
+ * of 128 x 128 outputs; N > 2^28 - 64 with up to 16 rows or with dbias; an FP32
+ * residual beside an FP8 output).
  * ---------------------------------------------------------------------- */
 typedef enum {
   FP8_ACT_NONE = 0, FP8_ACT_RELU = 1, FP8_ACT_GELU = 2, FP8_ACT_GELU_TANH = 3, FP8_ACT_SILU = 4

@@ -55,3 +55,31 @@ def test_product_plan(L):
     assert product(L, ask, K=100) == SHAPE and product(L, ask, act=9) == ARG and product(L, ask, aux=0x6001, ldaux=16) == ALIGN
     assert product(L, lambda g, e: L._L.fp8_scaled_gemm_ep_plan(g, e, None)) == NULL
     assert L._L.fp8_scaled_gemm_ep_plan(None, None, C.byref(plan)) == NULL
+
+
+def test_product_grids(L):
+    plan = L.EpPlan()
+
+    def ask(g, e):
+        return L._L.fp8_scaled_gemm_ep_plan(g, e, C.byref(plan))
+
+    # a launch's threads are counted in 32 bits, its workgroups in y in 16: the join
+    # of K parts takes 16 rows per workgroup
+    assert product(L, ask, 1048560, 1, 8192) == 0
+    for M, N, K in [(1048577, 1, 8192), (1048577, 1, 65536), (1100000, 1, 65536), (2000001, 128, 65536)]:
+        assert product(L, ask, M, N, K) == 0 and plan.k_parts == 1
+    n = (1 << 28) - 64
+    assert product(L, ask, 16, n, 128) == 0 and product(L, ask, 16, n + 1, 128) == UNSUPPORTED
+    assert product(L, ask, 17, n + 1, 128) == 0
+    assert product(L, ask, 17, n + 1, 128, backward=1, dbias=0x6000) == UNSUPPORTED
+    assert product(L, ask, 17, n, 128, backward=1, dbias=0x6000) == 0
+    assert product(L, ask, 128, 1 << 30, 128) == 0 and product(L, ask, 129, 1 << 30, 128) == UNSUPPORTED
+
+
+def test_product_inner_dimension(L):
+    def call(g, e):
+        return L._L.fp8_scaled_gemm_ep(g, e, None)
+
+    assert product(L, call, K=65552) == UNSUPPORTED and product(L, call, K=65536, lda=1 << 23) == UNSUPPORTED
+    plan = L.EpPlan()
+    assert product(L, lambda g, e: L._L.fp8_scaled_gemm_ep_plan(g, e, C.byref(plan)), K=65536) == 0
