@@ -25,7 +25,7 @@ fp8_status norm_common(const A& a) {
   if (a.gate_kind < FP8_GATE_NONE || a.gate_kind > FP8_GATE_FULL) return FP8_ERR_ARG;
   if (a.gate_act < FP8_GATE_LINEAR || a.gate_act > FP8_GATE_TANH) return FP8_ERR_ARG;
   if ((a.gate != nullptr) != (a.gate_kind != FP8_GATE_NONE) && a.rows > 0 && a.cols > 0) return FP8_ERR_ARG;
-  if (a.gate != nullptr && a.z == nullptr && a.rows > 0) return FP8_ERR_ARG;
+  if (a.gate != nullptr && a.z == nullptr && a.rows > 0 && a.cols > 0) return FP8_ERR_ARG;
   if (a.kind == FP8_NORM_RMS && a.b_post != nullptr) return FP8_ERR_ARG;
   if (a.cols > norm_max_cols()) return FP8_ERR_UNSUPPORTED;
   if (a.gate_kind == FP8_GATE_FULL && a.ldg < a.cols) return FP8_ERR_SHAPE;
@@ -125,7 +125,11 @@ fp8_status fp8_block_norm_bwd(const fp8_norm_bwd_args* args, hipStream_t stream)
   const fp8_status st = norm_common(a);
   if (st != FP8_OK) return st;
   if (a.kind == FP8_NORM_RMS && (a.db_pre != nullptr || a.db_post != nullptr)) return FP8_ERR_ARG;
-  if (a.cols == 0) return FP8_OK;
+  if (a.cols == 0) {   // a gate of each token is summed over no columns; every other output is empty
+    if (a.dgate == nullptr || a.gate_kind != FP8_GATE_TOKEN) return FP8_OK;
+    if (!aligned(a.dgate, 4)) return FP8_ERR_ALIGN;
+    return launched(launch_fill_u32(static_cast<uint32_t*>(a.dgate), a.rows, 0u, stream));
+  }
   const bool rows = a.rows > 0;
   // an output needs its input; without rows only the column sums are set, to 0
   if (rows) {

@@ -513,6 +513,7 @@ typedef enum { FP8_GATE_LINEAR = 0, FP8_GATE_SIGMOID = 1, FP8_GATE_TANH = 2 } fp
  *             FP8_SCALE_1x128: y8_scale_inv [ceil(cols/128)][rows], as
  *               fp8_cast_block.
  *   With neither y nor y8 only h is made (then z is required).
+ *   rows == 0 or cols == 0: nothing is written.
  * y is taken from h in binary32, before h is rounded to stream_dtype.  No
  * other output may overlap an input.
  * Errors: FP8_ERR_NULL (args, x, h with z, a scale), FP8_ERR_SHAPE (negative
@@ -551,7 +552,8 @@ fp8_status fp8_block_norm(const fp8_norm_args* args, hipStream_t stream);
  *            BF16, may be dy in place;  dgate: gate's shape and type ([rows][lddg]
  *            for FP8_GATE_FULL);  dw_pre, db_pre, dw_post, db_post [cols],
  *            param_dtype: overwritten.
- *   Each output is optional.  rows == 0 sets the column sums to 0.
+ *   Each output is optional.  rows == 0 sets the column sums to 0, cols == 0
+ *   a per-token dgate.
  *   workspace  fp8_block_norm_bwd_workspace(rows, cols) bytes (0 for sizes
  *            that the call refuses).
  * Errors: as fp8_block_norm; FP8_ERR_NULL also for the workspace,

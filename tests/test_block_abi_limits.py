@@ -83,3 +83,10 @@ def test_product_inner_dimension(L):
     assert product(L, call, K=65552) == UNSUPPORTED and product(L, call, K=65536, lda=1 << 23) == UNSUPPORTED
     plan = L.EpPlan()
     assert product(L, lambda g, e: L._L.fp8_scaled_gemm_ep_plan(g, e, C.byref(plan)), K=65536) == 0
+
+
+def test_norm_gradient_without_columns(L):
+    a = L.NormBwdArgs(rows=4, cols=0, kind=0, stream_dtype=0, param_dtype=1, gate=0x5000, gate_kind=2, dgate=0x6002)
+    assert L._L.fp8_block_norm_bwd(C.byref(a), None) == ALIGN
+    a.dgate = None
+    assert L._L.fp8_block_norm_bwd(C.byref(a), None) == 0

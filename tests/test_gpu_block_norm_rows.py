@@ -99,3 +99,15 @@ def test_backward(L, shape, kind, stream, gate):
             continue
         say(" ", n)
         R.close(o.t, want[n][0].reshape(o.t.shape), R.C * want[n][1].reshape(o.t.shape))
+
+
+def test_no_columns(L):
+    """The gradient of a gate per token is a sum over the columns: 0 without any."""
+    x, g = torch.empty((70, 0), device="cuda"), torch.ones((70, 1), device="cuda")
+    dg = Guarded((70, 1), F32)
+    dg.t.fill_(5.0)
+    L.fp8_block_norm_bwd(x, torch.empty_like(x), dh=x, z=x.to(BF), gate=g, dgate=dg.t, stats_z=torch.zeros((70, 2), device="cuda"))
+    torch.cuda.synchronize()
+    dg.check()
+    assert bool((dg.t == 0).all())
+    L.fp8_block_norm(x, z=x.to(BF), h=torch.empty_like(x), gate=g)   # and the pass itself has nothing to do
