@@ -369,20 +369,26 @@ __device__ __forceinline__ float gate_slope(int act, float value) {
 // The sigmoid forms cost one exponential and one reciprocal: with s(x) = 1 /
 // (1 + e^-x), SiLU is u s(u) and the tanh form of GELU u s(2 t), t = sqrt(2/pi)
 // (u + 0.044715 u^3), because 0.5 (1 + tanh t) = s(2 t); both slopes are
-// s + u s (1 - s) x'(u).  erf is formula 7.1.26 of Abramowitz and Stegun,
-// "Handbook of Mathematical Functions" (absolute error below 1.5e-7, a unit of
-// binary32 near 1): one reciprocal and e^(-u^2/2), which the slope needs too.
+// s + u s (1 - s) x'(u).  GELU's lower tail, erfc(x) / 2 with x = |u| / sqrt 2, is
+// e^(-x^2) t P(t), t = 1 / (1 + 0.43 x): P of degree 7 has the least largest relative
+// error over x = 0 .. 9.6 (beyond, e^(-x^2) is below 2^-132), 7e-8, so a value keeps its
+// digits however small it is (as 1 + erf(u / sqrt 2) it would lose them all by u = -5);
+// what is left is the rounding of the exponential's argument, 1.5 u^2 2^-24 of the
+// value.  One reciprocal, and e^(-u^2/2), which the slope needs too.
 constexpr float kRootTwoOverPi = 0.797884560802865f;
 template <bool SLOPE>
 __device__ __forceinline__ float gelu_erf(float u) {
   const float x = __builtin_fabsf(u) * 0.707106781186548f;
   const float e = __builtin_amdgcn_exp2f(-0.5f * kLog2E * u * u);
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
-  float q = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
-  q = __builtin_fmaf(t, q, 1.421413741f);
-  q = __builtin_fmaf(t, q, -0.284496736f);
-  q = __builtin_fmaf(t, q, 0.254829592f);
-  const float tail = 0.5f * q * t * e;               // 0.5 (1 - erf x)
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.43f, x, 1.0f));
+  float q = __builtin_fmaf(t, 0.0365416668f, -0.153960645f);
+  q = __builtin_fmaf(t, q, 0.189873412f);
+  q = __builtin_fmaf(t, q, -0.0411675461f);
+  q = __builtin_fmaf(t, q, 0.122594289f);
+  q = __builtin_fmaf(t, q, 0.102705248f);
+  q = __builtin_fmaf(t, q, 0.122154258f);
+  q = __builtin_fmaf(t, q, 0.12125928f);
+  const float tail = q * t * e;                      // 0.5 (1 - erf x)
   const float cdf = u < 0.0f ? tail : 1.0f - tail;   // 0.5 (1 + erf(u / sqrt 2))
   return SLOPE ? __builtin_fmaf(u * 0.398942280401433f, e, cdf) : u * cdf;
 }

@@ -1,0 +1,55 @@
+"""The functions inside the operators around the linears, one value at a time and
+relative to that value, where their 64-bit forms say how large it is: the tails
+of an activation, gates that are all but closed, turns next to a quarter.
+
+Bounds count roundings of binary32 (u = 2^-24, half a step).  The hardware
+exponential and reciprocal are within a step each (2 u)."""
+import math
+
+import pytest
+import torch
+
+from gpu_util import Guarded, say
+
+pytestmark = pytest.mark.gpu
+BF, F32, U8 = torch.bfloat16, torch.float32, torch.uint8
+u = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def L():
+    from fp8_mixed_precision_linear_amd import lib
+    return lib
+
+
+def norm_cdf(t):
+    return 0.5 * torch.special.erfc(-t * math.sqrt(0.5))
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_gelu_keeps_its_digits_in_the_tail(L, rows):
+    """GELU and its slope from -13 to 13.  The exponential's argument u^2 / 2 is
+    rounded three times (the constant, two products): 3 u^2 / 2 roundings of the
+    result; 24 more for the exponential, the reciprocal, a fit within 2 u, its
+    eight steps and the products around it."""
+    x = torch.cat([torch.linspace(-13, 13, 4096, device="cuda"), torch.tensor([-1e-6, 0.0, 1e-20, 30.0, 1e6], device="cuda")]).to(BF).float()
+    N = x.numel()
+    empty = torch.empty((rows, 0), dtype=U8, device="cuda")
+    D = Guarded((rows, N), F32)
+    L.fp8_scaled_gemm_ep(empty, 0, 0, None, torch.empty((N, 0), dtype=U8, device="cuda"), 0, 0, None, D.t, bias=x, act=L.ACT_GELU)
+    torch.cuda.synchronize()
+    D.check()
+    t = x.double()
+    want = t * norm_cdf(t)
+    assert bool(((D.t.double() - want).abs() <= (24 + 1.5 * t * t) * u * want.abs() + 2.0 ** -126).all())
+    # the slope: a product of ones (1 * 1 + 0 + ...), times act'(x)
+    A, B = torch.zeros((rows, 16), dtype=U8, device="cuda"), torch.zeros((N, 16), dtype=U8, device="cuda")
+    A[:, 0], B[:, 0] = 0x38, 0x38
+    one = torch.ones(1, device="cuda")
+    aux = x.to(BF).expand(rows, N).contiguous()
+    L.fp8_scaled_gemm_ep(A, 0, 0, one, B, 0, 0, one, D.t, act=L.ACT_GELU, aux=aux, backward=True)
+    torch.cuda.synchronize()
+    D.check()
+    pdf = torch.exp(-0.5 * t * t) / math.sqrt(2 * math.pi)
+    room = (24 + 1.5 * t * t) * u * (norm_cdf(t) + t.abs() * pdf) + 2.0 ** -126
+    assert bool(((D.t.double() - (norm_cdf(t) + t * pdf)).abs() <= room).all())
