@@ -84,9 +84,14 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeParams p) {
                         : p.pos_i64      ? reinterpret_cast<const int64_t*>(p.pos)[tok] + p.offset
                                          : (int64_t) reinterpret_cast<const int32_t*>(p.pos)[tok] + p.offset;
     const double turns = (double)pos * (p.freqs[i] * kInvTwoPi);
-    const float f = (float)(turns - rint(turns));
-    float s, c;
-    sincospif(2.0f * f, &s, &c);
+    // (the fraction's part beyond binary32 turns the result a little further: without it
+    // a cosine next to 0 would be off by up to 2^-23 and keep no digit)
+    const double part = turns - rint(turns);
+    const float f = (float)part, beyond = (float)((part - (double)f) * (1.0 / kInvTwoPi));
+    float s0, c0;
+    sincospif(2.0f * f, &s0, &c0);
+    float s = __builtin_fmaf(c0, beyond, s0);
+    const float c = __builtin_fmaf(-s0, beyond, c0);
     if (p.inverse) s = -s;
     cs[a] = make_float2(c * p.scale, s * p.scale);
   }

@@ -53,3 +53,24 @@ def test_gelu_keeps_its_digits_in_the_tail(L, rows):
     pdf = torch.exp(-0.5 * t * t) / math.sqrt(2 * math.pi)
     room = (24 + 1.5 * t * t) * u * (norm_cdf(t) + t.abs() * pdf) + 2.0 ** -126
     assert bool(((D.t.double() - (norm_cdf(t) + t * pdf)).abs() <= room).all())
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+def test_turns_keep_their_digits_next_to_a_quarter(L, inverse):
+    """Heads (1, 0) turned far into a context: cosine and sine within 3 steps of
+    themselves (two of the hardware's function, one of the correction), however
+    close to 0."""
+    T, n = 5000, 64
+    freqs = 10000.0 ** (-torch.arange(n, dtype=torch.float64, device="cuda") / n)
+    pos = torch.randint(0, 1 << 20, (T,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    q = torch.zeros((T, 1, 2 * n), device="cuda")
+    q[..., :n] = 1
+    L.fp8_rope(q, freqs, pos, inverse=inverse)
+    torch.cuda.synchronize()
+    # the turn's fraction, in 64 bits as the definition has it, then to a quarter: cos and sin of small angles
+    a = pos.double()[:, None] * freqs
+    c, s = a.cos(), a.sin() * (-1 if inverse else 1)
+    # (position times frequency in 64 bits leaves 2^-52 of up to 2^20 radians)
+    room = 2.0 ** -30
+    assert bool(((q[:, 0, :n].double() - c).abs() <= 6 * u * c.abs() + room).all())
+    assert bool(((q[:, 0, n:].double() - s).abs() <= 6 * u * s.abs() + room).all())
