@@ -539,9 +539,13 @@ __global__ void __launch_bounds__(ONE ? 512 : 1024) k_norm_bwd(NormGradParams p,
       }
     }
     if (!post) continue;
-    float gt = 1.0f;
+    float gt = 1.0f, gt_slope = 1.0f;
     if constexpr (EACH) {
-      if (p.gate_kind == 2 && live) gt = gate_value(p.gate_act, reinterpret_cast<const float*>(p.gate)[row]);
+      if (p.gate_kind == 2 && live) {
+        const float g = reinterpret_cast<const float*>(p.gate)[row];
+        gt = gate_value(p.gate_act, g);
+        gt_slope = gate_slope(p.gate_act, g);
+      }
     }
     // d becomes c = dn w_post; sums of c zh, c, and (EACH) dH n
     float q[EACH ? 3 : (LN ? 2 : 1)] = {};
@@ -572,14 +576,14 @@ __global__ void __launch_bounds__(ONE ? 512 : 1024) k_norm_bwd(NormGradParams p,
         if (p.gate_kind == 3) {
           if (live) load_vec<TINY>(row_of(p.gate, row, p.ldg, 0), 0, c.x[i], g);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) g[k] = gate_value(p.gate_act, g[k]);
+          for (int k = 0; k < 8; ++k) {
+            dg[k] = p.branch_scale * dg[k] * gate_slope(p.gate_act, g[k]);
+            g[k] = gate_value(p.gate_act, g[k]);
+          }
+          if (p.dgate) store_vec<TINY>(row_of(p.dgate, row, p.lddg, 0), 0, c.x[i], live, dg);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          dg[k] = p.branch_scale * dg[k] * gate_slope(p.gate_act, g[k]);
-          d[i][k] *= g[k];
-        }
-        if (p.dgate && p.gate_kind == 3) store_vec<TINY>(row_of(p.dgate, row, p.lddg, 0), 0, c.x[i], live, dg);
+        for (int k = 0; k < 8; ++k) d[i][k] *= g[k];
       }
       if constexpr (LN) add(3, i, d[i]);
 #pragma unroll
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(ONE ? 512 : 1024) k_norm_bwd(NormGradParams p,
     const float s0 = q[0] * inv_d, s1 = LN ? q[LN ? 1 : 0] * inv_d : 0.0f;
     if constexpr (EACH) {
       if (p.dgate && p.gate_kind == 2 && t == 0 && live)
-        reinterpret_cast<float*>(p.dgate)[row] = p.branch_scale * gate_slope(p.gate_act, gt) * q[EACH ? 2 : 0];
+        reinterpret_cast<float*>(p.dgate)[row] = p.branch_scale * gt_slope * q[EACH ? 2 : 0];
     }
     if (p.dz) {
 #pragma unroll
@@ -697,11 +701,12 @@ __global__ void __launch_bounds__(1024) k_norm_join(NormGradParams p, int nparts
   put(p.dw_pre, s[0]);
   if (ln) put(p.db_pre, s[1]);
   const float s1 = ln ? s[2] : s[1], s0 = ln ? s[3] : 0.0f;
-  const float g = p.gate_kind == 1 ? gate_value(p.gate_act, get(p.gate, 1.0f)) : 1.0f;
+  const float raw = p.gate_kind == 1 ? get(p.gate, 1.0f) : 1.0f;
+  const float g = p.gate_kind == 1 ? gate_value(p.gate_act, raw) : 1.0f;
   put(p.dw_post, p.branch_scale * g * s1);
   if (ln) put(p.db_post, p.branch_scale * g * s0);
   if (p.gate_kind == 1)
-    put(p.dgate, p.branch_scale * gate_slope(p.gate_act, g) *
+    put(p.dgate, p.branch_scale * gate_slope(p.gate_act, raw) *
                      (get(p.w_post, 1.0f) * s1 + (ln ? get(p.b_post, 0.0f) * s0 : 0.0f)));
 }
 

@@ -74,3 +74,29 @@ def test_turns_keep_their_digits_next_to_a_quarter(L, inverse):
     room = 2.0 ** -30
     assert bool(((q[:, 0, :n].double() - c).abs() <= 6 * u * c.abs() + room).all())
     assert bool(((q[:, 0, n:].double() - s).abs() <= 6 * u * s.abs() + room).all())
+
+
+@pytest.mark.parametrize("act", [1, 2])
+@pytest.mark.parametrize("gate", ["token", "channel"])
+def test_gate_gradients_keep_their_digits(L, act, gate):
+    """Gates from -12 to 12, through a sigmoid (1) or a tanh (2): the derivative
+    is e / (1 + e)^2 (times 4), e = exp(-|g|) (exp(-2 |g|)), to 12 roundings and
+    two of e's argument, beside the sums of 64 columns or rows."""
+    rows, cols = (513, 64) if gate == "token" else (64, 513)
+    g = torch.Generator(device="cuda").manual_seed(act)
+    z = torch.randn((rows, cols), generator=g, device="cuda").abs().add(0.5).to(BF)   # one sign: nothing cancels
+    dh = torch.rand((rows, cols), generator=g, device="cuda") + 0.5
+    x = torch.linspace(-12, 12, 513, device="cuda")
+    gate_t = x.view(rows, 1).contiguous() if gate == "token" else x
+    dg, dx = torch.empty_like(gate_t), torch.empty_like(dh)
+    rz = torch.rsqrt(z.double().square().mean(1, keepdim=True) + 1e-6)
+    stats = torch.cat([torch.zeros_like(rz), rz], 1).float()
+    L.fp8_block_norm_bwd(dh, dx, dh=dh, z=z, gate=gate_t, gate_act=act, stats_z=stats, dgate=dg)
+    torch.cuda.synchronize()
+    t = gate_t.double()
+    e = torch.exp(-t.abs() * (1 if act == 1 else 2))
+    slope = (1 if act == 1 else 4) * e / (1 + e) ** 2
+    n = z.double() * stats[:, 1:].double()
+    want = slope * (dh.double() * n).sum(1 if gate == "token" else 0, keepdim=gate == "token")
+    say(float(((dg.double() - want).abs() / want).max()))
+    assert bool(((dg.double() - want).abs() <= (12 + 64 + 4 * t.abs()) * u * want).all())
