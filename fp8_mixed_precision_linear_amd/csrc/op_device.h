@@ -343,29 +343,28 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 
 constexpr float kLog2E = 1.44269504088896f;
 
-// Gate G(g) and its derivative: 0 g itself, 1 sigmoid, 2 tanh.  With e = exp(-|g|),
-// the sigmoid is 1 / (1 + e), or e / (1 + e) for g < 0, and its derivative
-// e / (1 + e)^2; with e = exp(-2 |g|), tanh |g| = (1 - e) / (1 + e), which loses bits
-// where 1 - e cancels: below 1/4 the series to g^9 (the next term is below 2^-26 of it).
-// Its derivative is 4 e / (1 + e)^2: 1 - G^2, and G (1 - G) of the sigmoid, would lose
-// every digit for a gate that is all but open or shut.  (The compiler shares e and the
-// reciprocal between the two functions.)
-__device__ __forceinline__ float gate_exp(int act, float g) {
-  return __builtin_amdgcn_exp2f((act == 2 ? -2.0f * kLog2E : -kLog2E) * __builtin_fabsf(g));
-}
+// Gate G(g): 0 g itself, 1 sigmoid, 2 tanh.  With e = exp(-2 |g|), tanh |g| =
+// (1 - e) / (1 + e), which loses bits where 1 - e cancels: below 1/4 the series to
+// g^9 (the next term is below 2^-26 of it).
 __device__ __forceinline__ float gate_value(int act, float g) {
-  if (act == 0) return g;
-  const float e = gate_exp(act, g), r = __builtin_amdgcn_rcpf(1.0f + e);
-  if (act == 1) return g < 0.0f ? e * r : r;
-  const float q = g * g;
-  const float series = g * __builtin_fmaf(
-      q, __builtin_fmaf(q, __builtin_fmaf(q, __builtin_fmaf(q, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f),
-                        -1.0f / 3.0f), 1.0f);
-  return __builtin_fabsf(g) < 0.25f ? series : __builtin_copysignf((1.0f - e) * r, g);
+  if (act == 1) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * g));
+  if (act == 2) {
+    const float a = __builtin_fabsf(g), e = __builtin_amdgcn_exp2f(-2.0f * kLog2E * a), q = g * g;
+    const float series = g * __builtin_fmaf(
+        q, __builtin_fmaf(q, __builtin_fmaf(q, __builtin_fmaf(q, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f),
+                          -1.0f / 3.0f), 1.0f);
+    const float far = __builtin_copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), g);
+    return a < 0.25f ? series : far;
+  }
+  return g;
 }
+// Its derivative: e / (1 + e)^2 with e = exp(-|g|) for the sigmoid, 4 e / (1 + e)^2 with
+// e = exp(-2 |g|) for tanh.  G (1 - G) and 1 - G^2 would lose every digit for a gate
+// that is all but open or shut.
 __device__ __forceinline__ float gate_slope(int act, float g) {
   if (act == 0) return 1.0f;
-  const float e = gate_exp(act, g), r = __builtin_amdgcn_rcpf(1.0f + e);
+  const float e = __builtin_amdgcn_exp2f((act == 2 ? -2.0f * kLog2E : -kLog2E) * __builtin_fabsf(g));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
   return (act == 2 ? 4.0f : 1.0f) * e * r * r;
 }
 
