@@ -706,13 +706,16 @@ def fp8_rope_freqs(freqs, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, trained=
                              low, high, _stream(stream)))
 
 
-def _heads(t, shape, dtype, name):
-    """(pointer, token stride, head stride) of [tokens][heads][dim] heads."""
+def _heads(t, shape, dtype, name, written=False):
+    """(pointer, token stride, head stride) of [tokens][heads][dim] heads; heads
+    that are written may not share memory."""
     if t.dtype != dtype or t.shape != shape or not t.is_cuda:
         _refuse(t, shape, dtype, name)
     ts, hs, one = t.stride()
     if one != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have unit stride inside a head, got strides {t.stride()}")
+    if written and ((ts == 0 and shape[0] > 1) or (hs == 0 and shape[1] > 1)):
+        raise ValueError(f"{name} is written and must not be a broadcast view, got strides {t.stride()}")
     return t.data_ptr(), ts, hs
 
 
@@ -730,16 +733,16 @@ def fp8_rope(q, freqs, positions=None, k=None, q_out=None, k_out=None, layout=RO
     if len(shape) != 3:
         raise ValueError(f"q must be [tokens][heads][dim], got {tuple(shape)}")
     tokens, qh, dim = shape
-    qv = _heads(q, shape, dt, "q")
-    qo = qv if q_out is None else _heads(q_out, shape, dt, "q_out")
+    qv = _heads(q, shape, dt, "q", q_out is None)
+    qo = qv if q_out is None else _heads(q_out, shape, dt, "q_out", True)
     kh, kv, ko = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
         kshape = k.shape
         if len(kshape) != 3 or kshape[0] != tokens or kshape[2] != dim:
             raise ValueError(f"k must be [{tokens}][heads][{dim}], got {tuple(kshape)}")
         kh = kshape[1]
-        kv = _heads(k, kshape, dt, "k")
-        ko = kv if k_out is None else _heads(k_out, kshape, dt, "k_out")
+        kv = _heads(k, kshape, dt, "k", k_out is None)
+        ko = kv if k_out is None else _heads(k_out, kshape, dt, "k_out", True)
     pp, wide = 0, 0
     if positions is not None:
         wide = 1 if positions.dtype == torch.int64 else 0

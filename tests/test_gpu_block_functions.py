@@ -100,3 +100,22 @@ def test_gate_gradients_keep_their_digits(L, act, gate):
     want = slope * (dh.double() * n).sum(1 if gate == "token" else 0, keepdim=gate == "token")
     say(float(((dg.double() - want).abs() / want).max()))
     assert bool(((dg.double() - want).abs() <= (12 + 64 + 4 * t.abs()) * u * want).all())
+
+
+def test_broadcast_heads_are_read_but_not_written(L):
+    """A key head that several query heads share, as an expanded view: turned
+    into its own memory it is right, in place it would be turned once per head."""
+    x = torch.randn((20, 1, 16), device="cuda")
+    freqs = torch.linspace(1.0, 0.1, 8, dtype=torch.float64, device="cuda")
+    q, wide = torch.randn((20, 4, 16), device="cuda"), x.expand(20, 4, 16)
+    qo, ko, one = torch.empty_like(q), torch.empty_like(q), torch.empty_like(x)
+    L.fp8_rope(q, freqs, k=wide, q_out=qo, k_out=ko)
+    L.fp8_rope(x, freqs, q_out=one)
+    assert torch.equal(ko, one.expand(20, 4, 16))
+    before = x.clone()
+    for kw in (dict(k=wide, q_out=qo), dict(k=q, q_out=wide, k_out=ko)):
+        with pytest.raises(ValueError, match="broadcast"):
+            L.fp8_rope(q, freqs, **kw)
+    with pytest.raises(ValueError, match="broadcast"):
+        L.fp8_rope(x[:1].expand(20, 1, 16), freqs)
+    assert torch.equal(x, before)
