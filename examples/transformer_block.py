@@ -159,7 +159,8 @@ class Block:
         return dw
 
     def _transposed(self, y, scale):
-        """E4M3 codes [cols][rows] of an activation kept in bf16."""
+        """E4M3 codes [cols][rows] of an activation kept in bf16 (the norm writes
+        its codes row by row only, so a weight gradient's operand is a cast of its own)."""
         t = self._new(*y.shape[::-1], dtype=U8)
         L.fp8_cast_amax_acc(y, L.E4M3, scale, torch.zeros(1, device=self.device), None, t)
         return t

@@ -68,9 +68,11 @@ namespace {
 
 // Times (us) of one 128-byte step of K, measured with every compute unit busy: a
 // workgroup alone on its compute unit, and two of them (the 32-row tiles' stages
-// fill its LDS).  Without and with block scales; 256: the large kernels.  (The tiles'
+// fill its LDS).  Without and with block scales (measured with promoted ones, taken for
+// powers of two as well); 256: the large kernels with their own formats.  (The tiles'
 // steps with block scales have since become some 20% shorter; scaled by that, the
-// choices were 0.7% slower on average over 135 products, 19% at worst, so these stay.)
+// choices were 0.7% slower on average over 135 products, 19% at worst, so these stay:
+// they rank the cuts and no longer are what a step takes.)
 struct TileCost {
   int bm;
   float alone, two;

@@ -10,7 +10,9 @@
 // is rounded to the stream's type (the rounding would add its own half step
 // to y), and leaves as BF16 and / or as FP8 codes with the per-tensor scale of
 // the steps before, or the scale of the row or of each 128 columns of it:
-// the cast of the next linear's operand without a pass over y of its own.
+// the cast of the next linear's operand without a pass over y of its own.  (Codes
+// row by row: the transposed ones that a weight gradient multiplies are a cast of
+// their own.)
 //
 // Backward, from dy and dh (the gradient that reaches h from above):
 //   a = dy w_pre, xh = (h - mh) rh
@@ -24,16 +26,23 @@
 // S0 = sum_t dH give all of dw_post = bs G S1, db_post = bs G S0 and
 // dgate = bs G' (w S1 + b S0).
 //
-// Bound: HBM.  A row stays in registers between its loads and its stores, so
-// each element is read and written once; the column sums are kept in
-// registers over the rows that a workgroup takes and joined by a second, small
-// kernel in a fixed order (no atomics: equal inputs give equal bits).
+// Bound: HBM.  Up to 8192 columns, one vector of eight per thread, a row stays in
+// registers between its loads and its stores (but for up to 60 bytes per lane in some
+// kernels), so each element is read and written once; the column sums are kept in
+// registers or LDS over the rows that a workgroup takes and joined by a second, small
+// kernel in a fixed order (no atomics: equal inputs give equal bits).  Wider rows, with
+// two vectors per thread up to 16384 columns and four beyond, do not fit the 128
+// registers of a 1024-thread workgroup's threads: 64 .. 256 and 464 .. 880 bytes per lane
+// of the forward pass, 184 .. 648 and 1104 .. 1772 of the gradient wait in scratch
+// memory, and these are bound by that.
 //
 // Measured (MI355X, inputs that change from call to call; a copy of 2 x 2 GiB moves
 // 4.94 TB/s): 8192 x 8192 with channel gate and FP8 out 107 us, 4.4 TB/s; its gradient
-// 161 us, 5.0 TB/s, of which the join is 6; 1 x 8192 6.4 us of kernel; layer norm of
+// 160 us, 5.0 TB/s, of which the join is 6; 1 x 8192 6.4 us of kernel; layer norm of
 // 1531 x 2053 in binary32 17.4 us, 2.5 TB/s; gradient of 777 x 4095 33 us, 1.7 TB/s,
-// bound by its partial column sums.  Rows of an XCD kept contiguous: 5-8% slower.
+// bound by its partial column sums.  Wide rows: 4096 x 12288 138 us, gradient 232 (at 5
+// TB/s 81 and 121); 4096 x 16384 170 and 276 (107 and 161); 2048 x 28672 215 and 939 (94
+// and 141).  Rows of an XCD kept contiguous: 5-8% slower.
 #include <atomic>
 
 #include "op_device.h"

@@ -577,7 +577,8 @@ def fp8_block_norm(x, z=None, h=None, y=None, kind=NORM_RMS, eps=1e-6, w_pre=Non
     bf16 the output of the block that ends here (None: h is x), h the new
     stream (x's type; may be x).  y is bf16; y8 holds FP8 codes of y with
     y8_scaling SCALE_TENSOR (y8_scale given, y8_amax max-accumulated),
-    SCALE_ROW or SCALE_1x128 (y8_scale_inv written).  Weights and biases [cols]
+    SCALE_ROW or SCALE_1x128 (y8_scale_inv written), row by row (a transposed
+    copy is fp8_cast_*'s).  Weights and biases [cols]
     and a per-channel gate [cols] share one type; a gate [rows, 1] is float32, a
     gate [rows, cols] bf16.  stats_z / stats_h [rows, 2] float32 receive (mean,
     1 / deviation) for fp8_block_norm_bwd."""

@@ -466,8 +466,11 @@ fp8_status fp8_scaled_gemm(const fp8_gemm_args* args, hipStream_t stream);
  * The operators around the linears of a transformer block: norms with the
  * block's gate and residual scale, the GEMM with the linear's bias,
  * activation and residual, and rotary positions, each with its gradient.
- * They were added without changing any structure above, so the ABI version
- * stays.  Beyond the conventions at the top:
+ * They were added to version 10 without changing any structure or call above:
+ * the version alone does not tell a caller that they are there.  One that may
+ * meet an older library looks for the symbols (dlsym), one that is compiled
+ * against a header of unknown age for FP8LIN_BLOCK_OPERATORS.  Beyond the
+ * conventions at the top:
  *   - rows may be strided (ld >= columns, in elements); pointers need the
  *     alignment of their element only, unless stated otherwise;
  *   - an optional output or input is NULL when absent;
@@ -479,6 +482,7 @@ fp8_status fp8_scaled_gemm(const fp8_gemm_args* args, hipStream_t stream);
  * Every sum, norm statistic and column sum is held in binary32 and taken in
  * a fixed order: equal inputs on equal hardware give equal bits.
  * ===================================================================== */
+#define FP8LIN_BLOCK_OPERATORS 1
 typedef enum { FP8_DT_BF16 = 0, FP8_DT_F32 = 1 } fp8_dtype;
 typedef enum { FP8_NORM_RMS = 0, FP8_NORM_LAYER = 1 } fp8_norm_kind;
 /* Gate of a block's output: none, one value per channel [cols]
@@ -503,8 +507,8 @@ typedef enum { FP8_GATE_LINEAR = 0, FP8_GATE_SIGMOID = 1, FP8_GATE_TANH = 2 } fp
  *           belong to the layer norm only.
  *   stats_z, stats_h  [rows][2] FP32 (mean, rstd), for the gradient.
  *   y       [rows][ldy] BF16, and / or
- *   y8      [rows][ldy8] FP8 codes of y (of its binary32 value), y8_format,
- *           with y8_scaling
+ *   y8      [rows][ldy8] FP8 codes of y (of its binary32 value; row by row, no
+ *           transposed copy), y8_format, with y8_scaling
  *             FP8_SCALE_TENSOR: y8_scale (1 float) as in fp8_cast_e4m3 /
  *               e5m2; y8_amax (1 float, optional) is max-accumulated with
  *               max |y| as in fp8_amax_acc;
