@@ -435,10 +435,28 @@ struct EpWave {
 template <int NW>
 __device__ __forceinline__ void ep_amax(float* d_amax, uint32_t bits, int lane, int wave);
 
+// Columns of a product with two factors: 16 of the one, the same 16 of the other, and so
+// on.  Which factor and which of its columns column c stands for, and how many columns
+// n pairs take (a multiple of 32).
+__host__ __device__ constexpr int half_of(int c) { return (c >> 4) & 1; }
+__host__ __device__ constexpr int pair_of(int c) { return 16 * (c >> 5) + (c & 15); }
+__host__ __device__ constexpr int64_t paired_columns(int64_t n) { return (n + 15) / 16 * 32; }
+
+// What the kernels on tiles and on few rows are built around: the epilogue's
+// arguments, and who takes a wavefront's sums of WTN columns of B's rows.  PAIRED: B's
+// rows come in pairs of a product with two factors (gemm_gated.h).
+struct LinearOp {
+  using Params = EpParams;
+  static constexpr bool PAIRED = false;
+  template <int WTN, bool OUT8>
+  using Wave = EpWave<WTN, OUT8, EP_ANY, false>;
+};
+
 // The epilogue as the large kernels take it (FAST): accumulators of a wavefront whose
 // rows start at r0 and columns at c0; part: its row of column sums.
 template <int DIR>
 struct LinearEp {
+  static constexpr bool PAIRED = false;
   EpParams e;
   template <bool OUT8, int TI, int TJ, int NW, typename Deq>
   __device__ __forceinline__ void finish(const GemmParams& p, const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0,

@@ -35,23 +35,30 @@ __device__ __forceinline__ const float* scale_ptr(int scaling, const float* s, i
 }
 
 // BLOCK: block scales, promoted into binary32 per step;
-// SBCOL: B's differ by column (1x128 segments), else one per step.
-template <int AF, int BF, bool BLOCK, bool SBCOL, bool OUT8>
-__global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpParams e) {
+// SBCOL: B's differ by column (1x128 segments), else one per step.  OP: whose
+// epilogue; a PAIRED one's 32 columns are 16 rows of B's one factor and 16 of the
+// other, so a workgroup makes 16 outputs (one scale per step: of each factor).
+template <int AF, int BF, bool BLOCK, bool SBCOL, bool OUT8, typename OP = LinearOp>
+__global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, typename OP::Params e) {
   constexpr int NT = SK_COLS / 16, U = 4;
-  using W = EpWave<SK_COLS, OUT8, EP_ANY, false>;
+  constexpr bool PAIRED = OP::PAIRED;
+  using W = typename OP::template Wave<SK_COLS, OUT8>;
   constexpr int TS = 32, EPB = W::bytes(1), SUMS = 16 * SK_COLS * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[SK_WAVES * SUMS + EPB];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, l16 = lane & 15;
-  const int64_t M = p.M, N = p.N, n0 = (int64_t)blockIdx.x * SK_COLS;
+  const int64_t M = p.M, N = p.N, n0 = (int64_t)blockIdx.x * (PAIRED ? SK_COLS / 2 : SK_COLS);
+  auto b_row = [&](int c) -> int64_t {   // B's row of column c
+    if constexpr (PAIRED) return half_of(c) * N + min(n0 + pair_of(c), N - 1);
+    else return min(n0 + c, N - 1);
+  };
   const int nk = (int)((p.K + BK - 1) / BK), K = (int)p.K;
 
   const uint8_t* arow = p.A + min((int64_t)l16, M - 1) * p.lda + 16 * g;
   const uint8_t* brow[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) brow[j] = p.B + min(n0 + 16 * j + l16, N - 1) * p.ldb + 16 * g;
+  for (int j = 0; j < NT; ++j) brow[j] = p.B + b_row(16 * j + l16) * p.ldb + 16 * g;
   // block scales: A's of this lane's row, B's of its 4 columns or of the block
   const float* asc = nullptr;
   const float* bsc[NT][SBCOL ? 4 : 1];
@@ -62,7 +69,8 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int q = 0; q < (SBCOL ? 4 : 1); ++q)
-        bsc[j][q] = scale_ptr(p.b_scaling, p.b_sinv, N, SBCOL ? min(n0 + 16 * j + 4 * g + q, N - 1) : n0, bstep);
+        bsc[j][q] = scale_ptr(p.b_scaling, p.b_sinv, PAIRED ? 2 * N : N,
+                              SBCOL ? b_row(16 * j + 4 * g + q) : (PAIRED ? j * N + n0 : n0), bstep);
   }
 
   struct Step {
@@ -132,9 +140,9 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
   // scales, bias and residual are on their way before the wavefronts meet
   float* mine = reinterpret_cast<float*>(lds + wave * SUMS);
   uint32_t top = 0;
-  W w(p, e, n0, lane);
+  W w(p, e, (int64_t)blockIdx.x * SK_COLS, lane);
   static_assert(W::RPL == 1, "a lane has one row of 8 columns");
-  const int r = w.rg;
+  const int r = lane / (SK_COLS / 8), c8 = lane % (SK_COLS / 8);   // the row and 8 columns it adds up
   typename W::Words o[1];
   float sa = 0.0f, sb[8] = {};
   if (wave == 0) {
@@ -142,7 +150,7 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
     if (!BLOCK && K > 0) {
       sa = p.a_sinv[p.a_scaling == 5 ? min((int64_t)r, M - 1) : 0];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sb[k] = p.b_sinv[p.b_scaling == 5 ? min(w.c + k, N - 1) : 0];
+      for (int k = 0; k < 8; ++k) sb[k] = p.b_sinv[p.b_scaling == 5 ? b_row(8 * c8 + k) : 0];
     }
   }
 #pragma unroll
@@ -155,7 +163,7 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
     float v[8] = {};
 #pragma unroll
     for (int s = 0; s < SK_WAVES; ++s) {
-      const float4* q = reinterpret_cast<const float4*>(lds + s * SUMS) + (r * SK_COLS + 8 * w.cq) / 4;
+      const float4* q = reinterpret_cast<const float4*>(lds + s * SUMS) + (r * SK_COLS + 8 * c8) / 4;
       const float4 a = q[0], b = q[1];
       v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
       v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
@@ -164,12 +172,12 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = (v[k] * sa) * sb[k];
     }
-    *w.place(wl, w.rg, 2 * w.cq) = make_float4(v[0], v[1], v[2], v[3]);
-    *w.place(wl, w.rg, 2 * w.cq + 1) = make_float4(v[4], v[5], v[6], v[7]);
+    *w.place(wl, r, 2 * c8) = make_float4(v[0], v[1], v[2], v[3]);
+    *w.place(wl, r, 2 * c8 + 1) = make_float4(v[4], v[5], v[6], v[7]);
     w.stage(0, o, wl + W::src_at);
     w.template rows<TS>(0, wl, wl + W::src_at, wl + W::codes_at, 0);
     if constexpr (OUT8) {
-      if (p.D_t) w.template flush_t<TS, 16>(wl + W::codes_at, 0, n0);
+      if (p.D_t) w.template flush_t<TS, 16>(wl + W::codes_at, 0, (int64_t)blockIdx.x * SK_COLS);
     }
     w.put_dbias(0);
     top = w.amax_bits();
@@ -177,13 +185,16 @@ __global__ void __launch_bounds__(SK_WAVES * 64) k_ep_skinny(GemmParams p, EpPar
   if (p.d_amax) ep_amax<SK_WAVES>(p.d_amax, top, lane, wave);
 }
 
-template <int AF, int BF, bool OUT8>
-hipError_t launch_skinny_f(const GemmParams& p, const EpParams& e, hipStream_t s) {
-  const dim3 grid((unsigned)((p.N + SK_COLS - 1) / SK_COLS)), block(SK_WAVES * 64);
+template <int AF, int BF, bool OUT8, typename OP = LinearOp>
+hipError_t launch_skinny_f(const GemmParams& p, const typename OP::Params& e, hipStream_t s) {
+  const int64_t columns = OP::PAIRED ? paired_columns(p.N) : p.N;
+  const dim3 grid((unsigned)((columns + SK_COLS - 1) / SK_COLS)), block(SK_WAVES * 64);
   const bool blk = !((p.a_scaling == 0 || p.a_scaling == 5) && (p.b_scaling == 0 || p.b_scaling == 5));
-  if (!blk) hipLaunchKernelGGL((k_ep_skinny<AF, BF, false, false, OUT8>), grid, block, 0, s, p, e);
-  else if (p.b_scaling == 1) hipLaunchKernelGGL((k_ep_skinny<AF, BF, true, true, OUT8>), grid, block, 0, s, p, e);
-  else hipLaunchKernelGGL((k_ep_skinny<AF, BF, true, false, OUT8>), grid, block, 0, s, p, e);
+  // (16 columns of the second factor lie in one 128 x 128 block if it starts at a multiple of 16)
+  const bool by_column = p.b_scaling == 1 || (OP::PAIRED && p.b_scaling == 2 && p.N % 16 != 0);
+  if (!blk) hipLaunchKernelGGL((k_ep_skinny<AF, BF, false, false, OUT8, OP>), grid, block, 0, s, p, e);
+  else if (by_column) hipLaunchKernelGGL((k_ep_skinny<AF, BF, true, true, OUT8, OP>), grid, block, 0, s, p, e);
+  else hipLaunchKernelGGL((k_ep_skinny<AF, BF, true, false, OUT8, OP>), grid, block, 0, s, p, e);
   return hipGetLastError();
 }
 template <bool OUT8>

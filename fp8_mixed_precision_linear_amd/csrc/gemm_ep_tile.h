@@ -43,9 +43,13 @@ __device__ __forceinline__ int64_t scale_row(int scaling, int64_t row) {
   return scaling == 0 ? 0 : (scaling == 1 ? row : row / 128);
 }
 
-// WM x WN wavefronts of (16 TI) x (16 TJ).
-template <int AF, int BF, int MODE, bool OUT8, int WM, int WN, int TI, int TJ, int STAGES>
-__global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu(STAGES < 4 ? 2 : 1))) k_ep_tile(GemmParams p, EpParams e, int tiles_m, int tiles_n) {
+// WM x WN wavefronts of (16 TI) x (16 TJ).  OP: whose epilogue (LinearOp).  A PAIRED one's
+// B has 2 N rows, N of the one factor and N of the other, and a tile's BN columns are 16
+// of the one, 16 of the other and so on: column c of the tile stands for row
+// half(c) N + n0 + pair(c) of B.
+template <int AF, int BF, int MODE, bool OUT8, int WM, int WN, int TI, int TJ, int STAGES, typename OP = LinearOp>
+__global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu(STAGES < 4 ? 2 : 1))) k_ep_tile(GemmParams p, typename OP::Params e, int tiles_m, int tiles_n) {
+  constexpr bool PAIRED = OP::PAIRED;
   constexpr int BM_ = 16 * TI * WM, BN_ = 16 * TJ * WN;
   constexpr bool BLOCK = MODE != EP_SUM;
   static_assert(WM * WN == 4 && BM_ % 32 == 0 && BN_ % 32 == 0, "four wavefronts");
@@ -53,8 +57,9 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
   constexpr int SCALES = BLOCK ? 4 * ((BM_ + 63) / 64 * 64 + (BN_ + 63) / 64 * 64) : 0;
   constexpr int SA0 = ABYTES + BBYTES, SB0 = SA0 + (BM_ + 63) / 64 * 64 * 4;
   constexpr int STAGE_ = ABYTES + BBYTES + SCALES;
-  constexpr int WREG = EpWave<16 * TJ, OUT8, EP_ANY, false>::bytes(TI) > EpWave<16 * TJ, false, EP_ANY, false>::bytes(TI)
-                           ? EpWave<16 * TJ, OUT8, EP_ANY, false>::bytes(TI) : EpWave<16 * TJ, false, EP_ANY, false>::bytes(TI);
+  using W = typename OP::template Wave<16 * TJ, OUT8>;
+  constexpr int WREG = W::bytes(TI) > EpWave<16 * TJ, false, EP_ANY, false>::bytes(TI)
+                           ? W::bytes(TI) : EpWave<16 * TJ, false, EP_ANY, false>::bytes(TI);
   constexpr int LDS_ = STAGES * STAGE_ > 4 * WREG ? STAGES * STAGE_ : 4 * WREG;
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_];
   __shared__ float rs_tab[BLOCK ? 1 : BM_ + BN_];
@@ -71,10 +76,17 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
   const int group = bid / (GROUP_M * tiles_n), first_m = group * GROUP_M;
   const int gm = min(tiles_m - first_m, GROUP_M), in_group = bid - group * GROUP_M * tiles_n;
   const int tm = first_m + in_group % gm, tn = in_group / gm;
-  const int64_t m0 = (int64_t)tm * BM_, n0 = (int64_t)tn * BN_;
-  const int64_t rows_a = min((int64_t)BM_, M - m0), rows_b = min((int64_t)BN_, N - n0);
+  constexpr int BNP = PAIRED ? BN_ / 2 : BN_;
+  const int64_t m0 = (int64_t)tm * BM_, n0 = (int64_t)tn * BNP;
+  const int64_t rows_a = min((int64_t)BM_, M - m0), rows_b = min((int64_t)BNP, N - n0);
   const i32x4 ra = make_rsrc(p.A + m0 * p.lda, (uint32_t)(rows_a * p.lda));
   const i32x4 rb = make_rsrc(p.B + n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
+  const i32x4 rb2 = PAIRED ? make_rsrc(p.B + (N + n0) * p.ldb, (uint32_t)(rows_b * p.ldb)) : rb;
+  const int64_t brows = PAIRED ? 2 * N : N;
+  auto b_row = [&](int c) -> int64_t {   // B's row of the tile's column c, the last one's for those past it
+    if constexpr (PAIRED) return half_of(c) * N + min(n0 + pair_of(c), N - 1);
+    else return min(n0 + c, N - 1);
+  };
   const int lda = (int)p.lda, ldb = (int)p.ldb;
 
   // this workgroup's part of the K steps
@@ -95,11 +107,12 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
       const int ch = min(wave * PER + u, CA + CB - 1);
       const bool a = ch < CA;
       const int sc = a ? p.a_scaling : p.b_scaling, r = 64 * (a ? ch : ch - CA) + lane;
-      const int64_t rows = a ? M : N, r0 = a ? m0 : n0, first = scale_row(sc, r0), last = scale_row(sc, rows - 1);
+      const int64_t rows = a ? M : brows, r0 = a ? m0 : n0, first = scale_row(sc, r0), last = scale_row(sc, rows - 1);
       sc_base[u] = reinterpret_cast<const uint8_t*>((a ? p.a_sinv : p.b_sinv) + first);
       sc_step[u] = scale_base(sc, rows, 1) * 4;
-      sc_bytes[u] = (uint32_t)min(4 * (last - first + 1), (int64_t)2048);   // (at most 128 + 64 rows' are read)
-      sc_off[u] = (uint32_t)(4 * (min(scale_row(sc, r0 + r), last) - first));
+      // (at most 128 + 64 rows' are read, of each factor where there are two)
+      sc_bytes[u] = (uint32_t)min(4 * (last - first + 1), PAIRED ? (int64_t)1 << 30 : (int64_t)2048);
+      sc_off[u] = (uint32_t)(4 * (min(scale_row(sc, a ? m0 + r : b_row(r)), last) - first));
       sc_lds[u] = (uint32_t)((a ? SA0 : SB0) + 256 * (a ? ch : ch - CA));
     }
   }
@@ -115,7 +128,10 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
       const int kc = kb * BK + 16 * ((lane & 7) ^ swz(row));
       const uint32_t dst =
           base + (a ? 0 : ABYTES) + ((a ? (BM_ / 4) * wave + 8 * it : (BN_ / 4) * wave + 8 * (it - QA))) * BK;
-      dma16(dst, kc < (int)K ? (uint32_t)(row * (a ? lda : ldb)) + (uint32_t)kc : kOOB, a ? ra : rb);
+      const int src = a || !PAIRED ? row : pair_of(row);
+      static_assert(!PAIRED || BN_ % 128 == 0, "a wavefront's rows of B start at a pair's first");
+      dma16(dst, kc < (int)K ? (uint32_t)(src * (a ? lda : ldb)) + (uint32_t)kc : kOOB,
+            a ? ra : (PAIRED && half_of(8 * (it - QA)) ? rb2 : rb));
     }
     if constexpr (BLOCK) {
 #pragma unroll
@@ -133,7 +149,7 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
   if constexpr (!BLOCK) {
     for (int r = tid; r < BM_ + BN_; r += EP_THREADS) {
       const bool a = r < BM_;
-      const int64_t row = min((a ? m0 + r : n0 + r - BM_), (a ? M : N) - 1);
+      const int64_t row = a ? min(m0 + r, M - 1) : b_row(r - BM_);
       const bool per_row = (a ? p.a_scaling : p.b_scaling) == 5;
       rs_tab[r] = K > 0 ? (a ? p.a_sinv : p.b_sinv)[per_row ? row : 0] : 0.0f;
     }
@@ -148,8 +164,7 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
     if (kb0 + s < kb1) load(kb0 + s, s);
   // What the epilogue reads beside the product is on its way from here on: fetched
   // strip by strip after the sums, it held a 64 x 128 tile up by 4 us.
-  const int64_t r0 = m0 + wm * 16 * TI, c0 = n0 + wn * 16 * TJ;
-  using W = EpWave<16 * TJ, OUT8, EP_ANY, false>;
+  const int64_t r0 = m0 + wm * 16 * TI, c0 = (int64_t)tn * BN_ + wn * 16 * TJ;
   W w(p, e, c0, lane);
   constexpr int AHEAD = TI <= 2 ? TI : 1;
   typename W::Words src[AHEAD][W::RPL];
@@ -176,8 +191,9 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
     for (int j = 0; j < TJ; ++j) b[j] = frag(S + ABYTES, wn * 16 * TJ + 16 * j + l16, g);
     float4 sb[MODE == EP_BLKCOL ? TJ : 1];
     int eb[MODE == EP_MX ? TJ : 1];
-    float sb0 = 1.0f;
+    float sb0 = 1.0f, sb1 = 1.0f;   // (of the second factor's columns)
     if constexpr (MODE == EP_BLK) sb0 = *reinterpret_cast<const float*>(S + SB0);
+    if constexpr (MODE == EP_BLK && PAIRED) sb1 = *reinterpret_cast<const float*>(S + SB0 + 64);
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const uint8_t* at = S + SB0 + 4 * (wn * 16 * TJ + 16 * j);
@@ -190,6 +206,7 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
       const v8i a = frag(S, row, g);
       float sa = 1.0f;
       if constexpr (BLOCK) sa = *reinterpret_cast<const float*>(S + SA0 + 4 * row);
+      const float sa1 = sa * sb1;
       if constexpr (MODE == EP_BLK) sa *= sb0;
       const int ea = MODE == EP_MX ? (e8m0_of(sa) & keep_a) | one_a : 127;
 #pragma unroll
@@ -202,7 +219,7 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
           const v4f part = mfma<BF, AF>(b[j], a, v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if constexpr (MODE == EP_BLK) acc[i][j][q] = __builtin_fmaf(part[q], sa, acc[i][j][q]);
+            if constexpr (MODE == EP_BLK) acc[i][j][q] = __builtin_fmaf(part[q], PAIRED && (j & 1) ? sa1 : sa, acc[i][j][q]);
             else {
               const float c = q == 0 ? sb[j].x : (q == 1 ? sb[j].y : (q == 2 ? sb[j].z : sb[j].w));
               acc[i][j][q] = __builtin_fmaf(part[q] * sa, c, acc[i][j][q]);
@@ -234,6 +251,7 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
     ps.ldd = e.ldw;
     ps.d_f32 = 1;
     ps.d_amax = nullptr;
+    if constexpr (PAIRED) ps.N = paired_columns(N);
     EpWave<16 * TJ, false, EP_FWD, false> ws(ps, es, c0, lane);
     ws.template tile<TI, TJ>(acc, deq, r0, c0, wl);
     return;
@@ -243,14 +261,17 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
   if (p.d_amax) ep_amax<4>(p.d_amax, w.amax_bits(), lane, wave);
 }
 
-template <int AF, int BF, int MODE, bool OUT8>
-hipError_t launch_tile(const GemmParams& p, const EpParams& e, const EpPlan& plan, hipStream_t s) {
-  const int tiles_m = (int)((p.M + plan.bm - 1) / plan.bm), tiles_n = (int)((p.N + plan.bn - 1) / plan.bn);
+template <int AF, int BF, int MODE, bool OUT8, typename OP = LinearOp>
+hipError_t launch_tile(const GemmParams& p, const typename OP::Params& e, const EpPlan& plan, hipStream_t s) {
+  const int64_t columns = OP::PAIRED ? paired_columns(p.N) : p.N;
+  const int tiles_m = (int)((p.M + plan.bm - 1) / plan.bm), tiles_n = (int)((columns + plan.bn - 1) / plan.bn);
   const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)plan.splits), block(EP_THREADS);
 #define FP8LIN_TILE(...) \
-  hipLaunchKernelGGL((k_ep_tile<AF, BF, MODE, OUT8, __VA_ARGS__>), grid, block, 0, s, p, e, tiles_m, tiles_n)
-  if (plan.bm == 32) FP8LIN_TILE(1, 4, 2, 2, 6);
-  else if (plan.bm == 64) FP8LIN_TILE(2, 2, 2, 4, 3);
+  hipLaunchKernelGGL((k_ep_tile<AF, BF, MODE, OUT8, __VA_ARGS__, OP>), grid, block, 0, s, p, e, tiles_m, tiles_n)
+  if (plan.bm == 32) {
+    if constexpr (OP::PAIRED) FP8LIN_TILE(2, 2, 1, 4, 6);   // (a wavefront's 64 columns hold 32 pairs)
+    else FP8LIN_TILE(1, 4, 2, 2, 6);
+  } else if (plan.bm == 64) FP8LIN_TILE(2, 2, 2, 4, 3);
   else FP8LIN_TILE(2, 2, 4, 4, 2);
 #undef FP8LIN_TILE
   return hipGetLastError();

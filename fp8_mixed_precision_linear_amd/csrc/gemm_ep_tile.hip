@@ -200,12 +200,12 @@ hipError_t launch_gemm_ep(const GemmParams& p0, EpParams e, uint8_t* ws, hipStre
       if (err != hipSuccess) return err;
     }
   }
-  if (e.dbias) {
-    hipLaunchKernelGGL(k_ep_dbias, dim3((unsigned)((p.N + 63) / 64)), dim3(1024), 0, s, e.part, plan.parts, p.N,
-                       e.dbias, e.bias_f32);
-    return hipGetLastError();
-  }
-  return hipSuccess;
+  return e.dbias ? launch_ep_dbias(e.part, plan.parts, p.N, e.dbias, e.bias_f32, s) : hipSuccess;
+}
+
+hipError_t launch_ep_dbias(const float* part, int64_t parts, int64_t N, void* dbias, int f32, hipStream_t s) {
+  hipLaunchKernelGGL(k_ep_dbias, dim3((unsigned)((N + 63) / 64)), dim3(1024), 0, s, part, parts, N, dbias, f32);
+  return hipGetLastError();
 }
 
 }  // namespace fp8lin

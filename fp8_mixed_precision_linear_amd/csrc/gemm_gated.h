@@ -1,0 +1,498 @@
+// gemm_gated.h -- the gated pair of a feed-forward block as the epilogue of an FP8
+// product: what happens to a row of eight outputs, forward and backward, and how a
+// wavefront's sums become such rows.
+//
+// Forward, with g and u the two halves of a token's product (gate and up projection, in
+// binary32, biases added):  h = act(g) u;  D = h as BF16 or FP32, or as FP8 codes
+// encode(h * d_scale) with their transposed copy.  g and u may be kept, in BF16 or as a
+// checkpoint (checkpoint.h).
+// Backward, with v the product with the next linear's weights and g, u as kept:
+//   dg = v u act'(g),  du = v act(g);  D = (dg | du), dbias = their column sums.
+//
+// Forward the two factors of an output have to meet in one lane.  So B's rows are taken
+// 16 of the gate, the same 16 of the up projection, and so on (half_of, pair_of in
+// gemm_ep.h): the matrix instruction's column tiles alternate, and a strip of 16 rows in
+// LDS (see gemm_ep.h) holds both factors of the outputs.  A lane reads eight of each.
+// The checkpoint's blocks are 32 outputs of a row, four neighbouring lanes: no exchange
+// beyond a quad, and none between wavefronts.
+#pragma once
+
+#include "gemm_ep.h"
+#include "checkpoint.h"
+
+namespace fp8lin {
+
+namespace {
+
+// act(u) and act'(u), which share their exponential and reciprocal.
+__device__ __forceinline__ void act_and_slope(int act, const float (&u)[8], float (&a)[8], float (&s)[8]) {
+  if (act >= 3) {
+    const SigmoidForm f(act);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f.both(u[k], a[k], s[k]);
+  } else if (act == 2) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      a[k] = gelu_erf<false>(u[k]);
+      s[k] = gelu_erf<true>(u[k]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      a[k] = act == 1 && u[k] <= 0.0f ? 0.0f : u[k];
+      s[k] = act == 1 && !(u[k] > 0.0f) ? 0.0f : 1.0f;
+    }
+  }
+}
+
+// Eight values as FP8 codes of v * so.
+__device__ __forceinline__ void codes_of(int fp8, const float (&v)[8], float so, uint32_t& lo, uint32_t& hi) {
+  float x[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = v[k] * so;
+  if (fp8 == 1) encode8<0>(x, lo, hi);
+  else encode8<1>(x, lo, hi);
+}
+// Code k to the top of column k's word, the rows before down a byte.
+__device__ __forceinline__ void turn(uint32_t (&turned)[8], uint32_t lo, uint32_t hi) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    turned[k] = __builtin_amdgcn_perm(k < 4 ? lo : hi, turned[k], 0x00030201u | ((uint32_t)(4 + (k & 3)) << 24));
+}
+template <int RPL, int TS>
+__device__ __forceinline__ void put_turned(uint8_t* dst, const uint32_t (&turned)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if constexpr (RPL == 4) *reinterpret_cast<uint32_t*>(dst + k * TS) = turned[k];
+    else if constexpr (RPL == 2) *reinterpret_cast<uint16_t*>(dst + k * TS) = (uint16_t)(turned[k] >> 16);
+    else dst[k * TS] = (uint8_t)(turned[k] >> 24);
+  }
+}
+// Column-major codes of ROWS rows (TS bytes per column in LDS) to `cols` rows of D_t from
+// row n on, 16 bytes per lane; m: the first row, left: how many there are from it on.
+template <int TS, int ROWS>
+__device__ __forceinline__ void put_columns(uint8_t* d_t, int64_t ldt, const uint8_t* tl, int lane, int64_t n, int cols,
+                                            int64_t m, int64_t left) {
+  constexpr int LPC = ROWS / 16;
+  const int q = lane % LPC;
+  left -= 16 * q;
+  if (left <= 0) return;
+  uint8_t* dst = d_t + n * ldt + m + 16 * q;
+#pragma unroll 2
+  for (int k = lane / LPC; k < cols; k += 64 / LPC) {
+    const uint4 w = *reinterpret_cast<const uint4*>(tl + k * TS + 16 * q);
+    if (left >= 16) {
+      Pk16a1 a;
+      a.v[0] = w.x; a.v[1] = w.y; a.v[2] = w.z; a.v[3] = w.w;
+      *reinterpret_cast<Pk16a1*>(dst + k * ldt) = a;
+    } else {
+      for (int b = 0; b < (int)left; ++b) dst[k * ldt + b] = tl[k * TS + 16 * q + b];
+    }
+  }
+}
+
+// What both directions share: WTN columns in LDS, OC of them outputs of the wavefront,
+// lane's outputs c .. c + 7, RPL rows of a strip per lane (lanes past the strip's 16
+// rows are idle: on).  FAST as in gemm_ep.h.
+template <int WTN, int OC, bool OUT8, bool FAST>
+struct GatedBase {
+  static constexpr int LPR = OC / 8;
+  static constexpr int RPL = LPR >= 4 ? LPR / 4 : 1;
+  static constexpr int CH = WTN / 4;
+  static_assert(LPR == 2 || LPR == 4 || LPR == 8 || LPR == 16, "16, 32, 64 or 128 outputs");
+  const GemmParams& p;
+  const GatedParams& e;
+  int lane, cq, rg, nv;
+  bool on;
+  int64_t c;
+  uint32_t amax = 0;
+  float so;
+
+  __device__ __forceinline__ GatedBase(const GemmParams& p_, const GatedParams& e_, int64_t first, int lane_)
+      : p(p_), e(e_), lane(lane_), cq(lane_ % LPR), rg(lane_ / LPR), on(lane_ / LPR * RPL < 16),
+        c(first + 8 * (lane_ % LPR)) {
+    const int64_t left = p.N - c;
+    nv = !on ? 0 : left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+    if (!on) rg = 0;
+    so = OUT8 ? p.d_scale[0] : 1.0f;
+  }
+  __device__ __forceinline__ bool in(int k, int n) const { return FAST ? n > 0 : k < n; }
+
+  // Where the strip's row r keeps columns 4 q .. 4 q + 3.
+  static __device__ __forceinline__ float4* place(uint8_t* wl, int r, int q) {
+    return reinterpret_cast<float4*>(wl + r * (WTN * 4) + ((q ^ (r & (CH - 1))) << 4));
+  }
+  static __device__ __forceinline__ void read8(uint8_t* wl, int r, int q, float (&v)[8]) {
+    const float4 a = *place(wl, r, q), b = *place(wl, r, q + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  // Accumulators of strip i into LDS: lane (g, l16) has row l16, columns 16 j + 4 g .. + 3.
+  template <int TI, int TJ, int I, typename Deq>
+  __device__ __forceinline__ void spill(const v4f (&acc)[TI][TJ], Deq&& deq, uint8_t* wl) {
+    static_assert(16 * TJ == WTN, "the wavefront's columns");
+    const int g = lane >> 4, l16 = lane & 15;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+      *place(wl, l16, 4 * j + g) = make_float4(deq(I, j, 0, acc[I][j][0]), deq(I, j, 1, acc[I][j][1]),
+                                               deq(I, j, 2, acc[I][j][2]), deq(I, j, 3, acc[I][j][3]));
+  }
+  __device__ __forceinline__ void see(const float (&v)[8], int n) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) amax = max_u32(amax, in(k, n) ? abs_bits(v[k]) : 0u);
+  }
+  // max |d| of the wavefront as stored.
+  __device__ __forceinline__ uint32_t amax_bits() {
+    uint32_t a = wave_max(amax);
+    if (!OUT8 && !p.d_f32) a = (uint32_t)f32_to_bf16_rne(__uint_as_float(a)) << 16;
+    return a;
+  }
+  template <int B, int E, typename F>
+  static __device__ __forceinline__ void each(F&& f) {
+    if constexpr (B < E) {
+      f(std::integral_constant<int, B>{});
+      each<B + 1, E>(f);
+    }
+  }
+};
+
+// Forward: WTN columns of B's rows are WTN / 2 outputs.
+template <int WTN, bool OUT8, bool FAST>
+struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
+  using Base = GatedBase<WTN, WTN / 2, OUT8, FAST>;
+  using Base::LPR; using Base::RPL; using Base::p; using Base::e; using Base::lane; using Base::cq; using Base::rg;
+  using Base::nv; using Base::on; using Base::c; using Base::so; using Base::read8; using Base::in;
+  using Words = uint32_t;            // nothing is read beside the product
+  static constexpr int OC = WTN / 2;
+  static constexpr bool KEEPS = OC % 32 == 0;   // whole blocks of a checkpoint
+  static constexpr int src_at = 64 * WTN, codes_at = src_at;
+  static constexpr int bytes(int TI) { return codes_at + (OUT8 ? OC * (16 * TI + 16) : 0); }
+  float bias[2][8];
+
+  __device__ __forceinline__ GatedWave(const GemmParams& p_, const GatedParams& e_, int64_t n0, int lane_)
+      : Base(p_, e_, n0 / 2, lane_) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bias[0][k] = bias[1][k] = 0.0f;
+    if (e.bias) {
+      load8(e.bias, e.bias_f32, c, nv, bias[0]);
+      load8(e.bias, e.bias_f32, p.N + c, nv, bias[1]);
+    }
+  }
+  __device__ __forceinline__ void fetch(int64_t, Words (&)[RPL]) {}
+  __device__ __forceinline__ void stage(int64_t, const Words (&)[RPL], uint8_t*) {}
+
+  // The strip in wl, one row after the other (a loop that stays one: see EpWave).
+  template <int TS>
+  __device__ __forceinline__ void rows(int64_t m0, uint8_t* wl, const uint8_t*, uint8_t* tl, int tr) {
+    uint32_t turned[8] = {};
+    const int64_t first = m0 + rg * RPL;
+    const int esz = OUT8 ? 1 : (p.d_f32 ? 4 : 2);
+    char* d = reinterpret_cast<char*>(p.D) + (first * p.ldd + c) * esz;
+    const int64_t F = p.N, nb = ck_blocks(F);
+#pragma unroll 1
+    for (int t = 0; t < RPL; ++t) {
+      const int64_t m = first + t;
+      const int n = m < p.M ? nv : 0;
+      const int q = 8 * (cq >> 1) + 2 * (cq & 1);
+      float g[8], u[8], v[8];
+      read8(wl, rg * RPL + t, q, g);
+      read8(wl, rg * RPL + t, q + 4, u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        g[k] += bias[0][k];
+        u[k] += bias[1][k];
+      }
+      if (e.aux) {
+        uint16_t* a = reinterpret_cast<uint16_t*>(e.aux) + m * e.ldaux + c;
+        put8<LPR, FAST>(a, 0, n, g);
+        put8<LPR, FAST>(a + F, 0, n, u);
+      }
+      if constexpr (KEEPS) {
+        if (e.ck) {
+          uint8_t* a = e.ck + m * e.ldck + c;
+          uint8_t* x = e.ck_exp + m * e.ldexp + (c >> 5);
+          keep(g, n, a, x);
+          keep(u, n, a + F, x + nb);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = g[k];
+      activate<false>(e.act, v, g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= u[k];
+      if (p.d_amax) this->see(v, n);
+      if constexpr (OUT8) {
+        uint32_t lo, hi;
+        codes_of(p.d_fp8, v, so, lo, hi);
+        put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
+        if (p.D_t) turn(turned, lo, hi);
+      } else {
+        put8<LPR, FAST>(d, p.d_f32, n, v);
+      }
+      d += p.ldd * esz;
+    }
+    if constexpr (OUT8) {
+      if (p.D_t && on) put_turned<RPL, TS>(tl + (8 * cq) * TS + tr + rg * RPL, turned);
+    }
+    asm volatile("" ::: "memory");   // LDS is written and read as different types
+  }
+
+  // Eight values of a block's 32 to the checkpoint.
+  __device__ __forceinline__ void keep(const float (&v)[8], int n, uint8_t* ck, uint8_t* exp) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a = max_u32(a, in(k, n) ? abs_bits(v[k]) : 0u);
+    a = max_u32(a, dpp<kXor1>(a));
+    a = max_u32(a, dpp<kXor2>(a));
+    const uint32_t byte = ck_exponent(a);
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = v[k] * ck_scale(byte);
+    uint32_t lo, hi;
+    encode8<0>(x, lo, hi);
+    put8_codes<LPR, FAST>(ck, n, lo, hi);
+    if ((cq & 3) == 0 && n > 0) *exp = (uint8_t)byte;
+  }
+
+  template <int TI, int TJ, typename Deq>
+  __device__ __forceinline__ void tile(const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t n0, uint8_t* wl) {
+    constexpr int TS = 16 * TI + 16;
+    this->template each<0, TI>([&](auto itag) {
+      constexpr int i = decltype(itag)::value;
+      this->template spill<TI, TJ, i>(acc, deq, wl);
+      rows<TS>(r0 + 16 * i, wl, nullptr, wl + codes_at, 16 * i);
+    });
+    if constexpr (OUT8) {
+      if (p.D_t) flush_t<TS, 16 * TI>(wl + codes_at, r0, n0);
+    }
+  }
+  template <int TI, int TJ, int STRIPS, typename Deq>
+  __device__ __forceinline__ void tile(const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t n0, uint8_t* wl,
+                                       Words (&)[STRIPS][RPL]) {
+    tile(acc, deq, r0, n0, wl);
+  }
+  template <int TS, int ROWS>
+  __device__ __forceinline__ void flush_t(const uint8_t* tl, int64_t r0, int64_t n0) {
+    const int64_t first = n0 / 2, cols = p.N - first;
+    put_columns<TS, ROWS>(p.D_t, p.ldt, tl, lane, first, cols < OC ? (int)cols : OC, r0, p.M - r0);
+  }
+  __device__ __forceinline__ void put_dbias(int64_t) {}
+};
+
+// Backward.  KEPT: g and u come from BF16 (0), from a checkpoint (1), or from either (2).
+template <int WTN, bool OUT8, bool FAST, int KEPT>
+struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
+  using Base = GatedBase<WTN, WTN, OUT8, FAST>;
+  using Base::LPR; using Base::RPL; using Base::p; using Base::e; using Base::lane; using Base::cq; using Base::rg;
+  using Base::nv; using Base::c; using Base::so; using Base::read8; using Base::in;
+  static_assert(LPR >= 4, "whole strips");
+  struct Words { v8u g, u; };
+  // LDS: the strip, each lane's own words of g and u (32 bytes a row), and (OUT8) the
+  // column-major codes of dg and du of two strips, which leave 32 bytes a column: all
+  // of a wavefront's eight would take more than its part of the stages.
+  static constexpr int FLUSH = 2, TS_ = 16 * FLUSH + 16;
+  static constexpr int src_at = 64 * WTN, codes_at = src_at + RPL * 64 * 32;
+  static constexpr int bytes(int) { return codes_at + (OUT8 ? 2 * WTN * TS_ : 0); }
+  float db[2][8];
+
+  __device__ __forceinline__ GatedGradWave(const GemmParams& p_, const GatedParams& e_, int64_t n0, int lane_)
+      : Base(p_, e_, n0, lane_) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) db[0][k] = db[1][k] = 0.0f;
+  }
+  __device__ __forceinline__ bool coded() const { return KEPT == 2 ? e.ck != nullptr : KEPT == 1; }
+
+  // The strip of rows m0 .. m0 + 15 of g and u, in flight until stage().
+  __device__ __forceinline__ void fetch(int64_t m0, Words (&o)[RPL]) {
+#pragma unroll
+    for (int t = 0; t < RPL; ++t) {
+      const int64_t m = m0 + rg * RPL + t;
+      const int n = m < p.M ? nv : 0;
+      if (coded()) {
+        const uint8_t* a = e.ck + m * e.ldck + c;
+        const uint8_t* x = e.ck_exp + m * e.ldexp + (c >> 5);
+        load_codes(a, n, o[t].g);
+        load_codes(a + p.N, n, o[t].u);
+        if (n > 0) {
+          o[t].g[2] = x[0];
+          o[t].u[2] = x[ck_blocks(p.N)];
+        }
+      } else {
+        const uint16_t* a = reinterpret_cast<const uint16_t*>(e.aux) + m * e.ldaux + c;
+        load_packed<FAST, false>(a, 0, n, o[t].g);
+        load_packed<FAST, false>(a + p.N, 0, n, o[t].u);
+      }
+    }
+  }
+  static __device__ __forceinline__ void load_codes(const uint8_t* a, int n, v8u& w) {
+    if (n <= 0) return;
+    if (FAST || n >= 8) {
+      struct __attribute__((packed, aligned(FAST ? 4 : 1))) Two { uint32_t a, b; };
+      const Two q = *reinterpret_cast<const Two*>(a);
+      w[0] = q.a;
+      w[1] = q.b;
+    } else {
+      uint32_t d[2] = {0u, 0u};
+#pragma unroll
+      for (int k = 0; k < 7; ++k)
+        if (k < n) d[k >> 2] |= (uint32_t)a[k] << (8 * (k & 3));
+      w[0] = d[0];
+      w[1] = d[1];
+    }
+  }
+  // Each lane's own words: 16 bytes of g's eight values and 16 of u's a row, or 16 of
+  // both's codes and exponents.
+  __device__ __forceinline__ void stage(int64_t m0, const Words (&o)[RPL], uint8_t* ol) {
+    uint4* q = reinterpret_cast<uint4*>(ol) + lane;
+#pragma unroll
+    for (int t = 0; t < RPL; ++t) {
+      if (coded()) {
+        q[t * 64] = make_uint4(o[t].g[0], o[t].g[1], o[t].u[0], o[t].u[1]);
+        reinterpret_cast<uint32_t*>(ol + RPL * 64 * 16)[t * 64 + lane] = o[t].g[2] | (o[t].u[2] << 8);
+      } else {
+        const uint16_t* a = reinterpret_cast<const uint16_t*>(e.aux) + (m0 + rg * RPL + t) * e.ldaux + c;
+        q[t * 64] = words(o[t].g, FAST ? 0u : odd_of(a));
+        q[(RPL + t) * 64] = words(o[t].u, FAST ? 0u : odd_of(a + p.N));
+      }
+    }
+  }
+  static __device__ __forceinline__ uint4 words(const v8u& w, uint32_t s) {
+    if (FAST) return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(__builtin_amdgcn_alignbyte(w[1], w[0], s), __builtin_amdgcn_alignbyte(w[2], w[1], s),
+                      __builtin_amdgcn_alignbyte(w[3], w[2], s), __builtin_amdgcn_alignbyte(w[4], w[3], s));
+  }
+  static __device__ __forceinline__ void widen(const uint4& a, float (&v)[8]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = bf16_lo(w[k]);
+      v[2 * k + 1] = bf16_hi(w[k]);
+    }
+  }
+
+  template <int TS>
+  __device__ __forceinline__ void rows(int64_t m0, uint8_t* wl, const uint8_t* ol, uint8_t* tl, int tr) {
+    uint32_t tg[8] = {}, tu[8] = {};
+    const int64_t first = m0 + rg * RPL;
+    const int esz = OUT8 ? 1 : (p.d_f32 ? 4 : 2);
+    char* d = reinterpret_cast<char*>(p.D) + (first * p.ldd + c) * esz;
+    const int64_t half = p.N * esz;
+    const uint4* q = reinterpret_cast<const uint4*>(ol) + lane;
+#pragma unroll 1
+    for (int t = 0; t < RPL; ++t) {
+      const int n = first + t < p.M ? nv : 0;
+      float v[8], g[8], u[8], a[8], s[8];
+      read8(wl, rg * RPL + t, 2 * cq, v);
+      const uint4 x = q[t * 64];
+      if (coded()) {
+        const uint32_t b = reinterpret_cast<const uint32_t*>(ol + RPL * 64 * 16)[t * 64 + lane];
+        ck_values(x.x, x.y, b & 0xFFu, g);
+        ck_values(x.z, x.w, b >> 8, u);
+      } else {
+        widen(x, g);
+        widen(q[(RPL + t) * 64], u);
+      }
+      act_and_slope(e.act, g, a, s);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        g[k] = v[k] * u[k] * s[k];
+        u[k] = v[k] * a[k];
+      }
+      if (e.dbias) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          db[0][k] += in(k, n) ? g[k] : 0.0f;
+          db[1][k] += in(k, n) ? u[k] : 0.0f;
+        }
+      }
+      if (p.d_amax) {
+        this->see(g, n);
+        this->see(u, n);
+      }
+      if constexpr (OUT8) {
+        uint32_t lo, hi;
+        codes_of(p.d_fp8, g, so, lo, hi);
+        put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
+        if (p.D_t) turn(tg, lo, hi);
+        codes_of(p.d_fp8, u, so, lo, hi);
+        put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d) + half, n, lo, hi);
+        if (p.D_t) turn(tu, lo, hi);
+      } else {
+        put8<LPR, FAST>(d, p.d_f32, n, g);
+        put8<LPR, FAST>(d + half, p.d_f32, n, u);
+      }
+      d += p.ldd * esz;
+    }
+    if constexpr (OUT8) {
+      if (p.D_t) {
+        uint8_t* dst = tl + (8 * cq) * TS + tr + rg * RPL;
+        put_turned<RPL, TS>(dst, tg);
+        put_turned<RPL, TS>(dst + WTN * TS, tu);
+      }
+    }
+    asm volatile("" ::: "memory");   // LDS is written and read as different types
+  }
+
+  template <int TI, int TJ, typename Deq>
+  __device__ __forceinline__ void tile(const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t n0, uint8_t* wl) {
+    Words o[1][RPL];
+    fetch(r0, o[0]);
+    tile(acc, deq, r0, n0, wl, o);
+  }
+  template <int TI, int TJ, int STRIPS, typename Deq>
+  __device__ __forceinline__ void tile(const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t n0, uint8_t* wl,
+                                       Words (&o)[STRIPS][RPL]) {
+    static_assert(STRIPS == 1 || STRIPS == TI, "one strip ahead, or all");
+    this->template each<0, TI>([&](auto itag) {
+      constexpr int i = decltype(itag)::value;
+      this->template spill<TI, TJ, i>(acc, deq, wl);
+      stage(r0 + 16 * i, o[STRIPS == 1 ? 0 : i], wl + src_at);
+      if constexpr (STRIPS == 1 && i + 1 < TI) fetch(r0 + 16 * (i + 1), o[0]);
+      rows<TS_>(r0 + 16 * i, wl, wl + src_at, wl + codes_at, 16 * (i % FLUSH));
+      if constexpr (OUT8) {
+        if (p.D_t) {
+          if constexpr (i % FLUSH == FLUSH - 1) flush_t<TS_, 16 * FLUSH>(wl + codes_at, r0 + 16 * (i - FLUSH + 1), n0);
+          else if constexpr (i == TI - 1) flush_t<TS_, 16 * (TI % FLUSH)>(wl + codes_at, r0 + 16 * (TI - TI % FLUSH), n0);
+        }
+      }
+    });
+  }
+  template <int TS, int ROWS>
+  __device__ __forceinline__ void flush_t(const uint8_t* tl, int64_t r0, int64_t n0) {
+    const int cols = p.N - n0 < WTN ? (int)(p.N - n0) : WTN;
+    put_columns<TS, ROWS>(p.D_t, p.ldt, tl, lane, n0, cols, r0, p.M - r0);
+    put_columns<TS, ROWS>(p.D_t, p.ldt, tl + WTN * TS, lane, p.N + n0, cols, r0, p.M - r0);
+    asm volatile("" ::: "memory");
+  }
+
+  // Column sums of the wavefront's rows to part[row][2 N] (see EpWave).
+  __device__ __forceinline__ void put_dbias(int64_t row) {
+    if (e.dbias == nullptr) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int off = LPR; off < 64; off <<= 1) db[h][k] += __shfl_xor(db[h][k], off, 64);
+      if (rg == 0 && nv > 0) store8(e.part, 1, (2 * row + h) * p.N + c, nv, db[h]);
+    }
+  }
+};
+
+// What the tile and few-row kernels are built around (LinearOp in gemm_ep.h).
+struct GatedOp {
+  using Params = GatedParams;
+  static constexpr bool PAIRED = true;
+  template <int WTN, bool OUT8>
+  using Wave = GatedWave<WTN, OUT8, false>;
+};
+struct GatedGradOp {
+  using Params = GatedParams;
+  static constexpr bool PAIRED = false;
+  template <int WTN, bool OUT8>
+  using Wave = GatedGradWave<WTN, OUT8, false, 2>;
+};
+
+}  // namespace
+
+}  // namespace fp8lin

@@ -1,0 +1,16 @@
+// gemm_gated_skinny.hip -- the few-row kernel (gemm_ep_skinny.h) with the gated pair's
+// epilogue, both directions.
+#include "gemm_ep_skinny.h"
+#include "gemm_gated.h"
+
+namespace fp8lin {
+
+hipError_t launch_gated_skinny(const GemmParams& p, const GatedParams& e, hipStream_t s) {
+  if (!e.backward)
+    return p.d_fp8 ? launch_skinny_f<0, 0, true, GatedOp>(p, e, s) : launch_skinny_f<0, 0, false, GatedOp>(p, e, s);
+  if (p.a_fmt == 0)
+    return p.d_fp8 ? launch_skinny_f<0, 0, true, GatedGradOp>(p, e, s) : launch_skinny_f<0, 0, false, GatedGradOp>(p, e, s);
+  return p.d_fp8 ? launch_skinny_f<1, 0, true, GatedGradOp>(p, e, s) : launch_skinny_f<1, 0, false, GatedGradOp>(p, e, s);
+}
+
+}  // namespace fp8lin

@@ -216,5 +216,39 @@ hipError_t launch_gemm_ep_tile_blk_fp8out(const GemmParams& p, const EpParams& e
 hipError_t launch_gemm_ep_skinny(const GemmParams& p, const EpParams& e, hipStream_t s);
 hipError_t launch_gemm_ep_skinny_fp8out(const GemmParams& p, const EpParams& e, hipStream_t s);
 hipError_t launch_gemm_ep(const GemmParams& p, EpParams e, uint8_t* ws, hipStream_t s);
+// dbias[n] = sum over `parts` rows of column sums part[parts][N], in a fixed order.
+hipError_t launch_ep_dbias(const float* part, int64_t parts, int64_t N, void* dbias, int f32, hipStream_t s);
+
+// The gated pair of a feed-forward block (gemm_gated*.hip).  p.N = F, the outputs per
+// token; forward, B has 2 F rows; backward, D has 2 F columns.
+struct GatedParams {
+  int backward, act, bias_f32, splits;
+  const void* bias;   // forward: [2 F]
+  void* aux;          // [M][2 F] bf16: forward written, backward read
+  int64_t ldaux;
+  uint8_t* ck;        // the same as a checkpoint (checkpoint.h), each half by itself
+  int64_t ldck;
+  uint8_t* ck_exp;    // [M][2 ceil(F / 32)]
+  int64_t ldexp;
+  void* dbias;        // backward: [2 F]
+  float* part;        // workspace: column sums
+  float* sums;        // workspace: [splits][M][ldw]
+  int64_t ldw;
+};
+// What the workspace has to allow for, and what a call takes.
+EpPlan gated_plan(const GemmParams& p, int backward);
+EpPlan gated_plan(const GemmParams& p, const GatedParams& e);
+hipError_t launch_gated(const GemmParams& p, GatedParams e, uint8_t* ws, hipStream_t s);
+hipError_t launch_gated_tile(const GemmParams& p, const GatedParams& e, const EpPlan& plan, hipStream_t s);
+hipError_t launch_gated_tile_blk(const GemmParams& p, const GatedParams& e, const EpPlan& plan, hipStream_t s);
+hipError_t launch_gated_grad_tile(const GemmParams& p, const GatedParams& e, const EpPlan& plan, hipStream_t s);
+hipError_t launch_gated_grad_tile_blk(const GemmParams& p, const GatedParams& e, const EpPlan& plan, hipStream_t s);
+hipError_t launch_gated_skinny(const GemmParams& p, const GatedParams& e, hipStream_t s);
+
+// 8-bit checkpoints (checkpoint_kernels.hip).
+hipError_t launch_checkpoint_save(const void* x, int f32, int64_t rows, int64_t cols, int64_t ldx, uint8_t* ck,
+                                  int64_t ldck, uint8_t* ck_exp, int64_t ldexp, hipStream_t s);
+hipError_t launch_checkpoint_load(const uint8_t* ck, int64_t ldck, const uint8_t* ck_exp, int64_t ldexp, int64_t rows,
+                                  int64_t cols, void* y, int f32, int64_t ldy, hipStream_t s);
 
 }  // namespace fp8lin

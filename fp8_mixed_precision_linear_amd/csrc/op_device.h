@@ -416,6 +416,13 @@ struct SigmoidForm {
     const float q = u * u, s = sigmoid(u, q);
     return __builtin_fmaf(u * (s - s * s), __builtin_fmaf(3.0f * b, q, a), s);
   }
+  // Both, from one sigmoid.
+  __device__ __forceinline__ void both(float u, float& value, float& slope) const {
+    const float q = __builtin_fminf(u * u, 1e30f), s = sigmoid(u, q);
+    const float x = u == u ? __builtin_amdgcn_fmed3f(u, -100.0f, 100.0f) : u;
+    value = u * s;
+    slope = __builtin_fmaf(x * (s - s * s), __builtin_fmaf(3.0f * b, x * x, a), s);
+  }
 };
 
 }  // namespace

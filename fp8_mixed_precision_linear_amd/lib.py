@@ -96,6 +96,13 @@ class EpPlan(C.Structure):
     _fields_ = [("kernel", C.c_int), ("tile_rows", C.c_int), ("k_parts", C.c_int)]
 
 
+class GatedArgs(C.Structure):
+    _fields_ = [("backward", C.c_int), ("act", C.c_int), ("param_dtype", C.c_int), ("bias", C.c_void_p),
+                ("aux", C.c_void_p), ("ldaux", C.c_int64), ("ck", C.c_void_p), ("ldck", C.c_int64),
+                ("ck_exp", C.c_void_p), ("ldexp", C.c_int64), ("dbias", C.c_void_p),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
+
+
 class RopeArgs(C.Structure):
     _fields_ = [("tokens", C.c_int64), ("q_heads", C.c_int64), ("k_heads", C.c_int64),
                 ("dim", C.c_int64), ("pairs", C.c_int64),
@@ -140,6 +147,11 @@ def _load():
         "fp8_scaled_gemm_ep_workspace": (i64, [i64, i64, i64, i32, i32]),
         "fp8_scaled_gemm_ep": (i32, [vp, vp, vp]),
         "fp8_scaled_gemm_ep_plan": (i32, [vp, vp, vp]),
+        "fp8_gated_linear_workspace": (i64, [i64, i64, i64, i32, i32, i32]),
+        "fp8_gated_linear": (i32, [vp, vp, vp]),
+        "fp8_gated_linear_plan": (i32, [vp, vp, vp]),
+        "fp8_checkpoint_save": (i32, [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp]),
+        "fp8_checkpoint_load": (i32, [vp, i64, vp, i64, i64, i64, vp, i32, i64, vp]),
         "fp8_rope": (i32, [vp, vp]),
         "fp8_rope_freqs": (i32, [vp, i64, C.c_double, i32, C.c_double, C.c_double, C.c_double, C.c_double, vp]),
     }
@@ -464,6 +476,7 @@ _pack_gemm = _packer("qqqqqqPiiPPiiPPiPiPPqi", GemmArgs)
 _pack_norm = _packer("qqiiifffPqPqPPPPPqiiPqPPPqPqiiPPP", NormArgs)
 _pack_norm_bwd = _packer("qqiiiffPqPqPqPPqPPPPPqiiPqPqPqPPPPPq", NormBwdArgs)
 _pack_ep = _packer("iiiPPqifPqPPq", EpilogueArgs)
+_pack_gated = _packer("iiiPPqPqPqPPq", GatedArgs)
 _pack_rope = _packer("qqqqqiiifPPiqPqqPqqPqqPqq", RopeArgs)
 
 
@@ -695,6 +708,97 @@ def fp8_scaled_gemm_ep(A, a_fmt, a_scaling, a_scale_inv, B, b_fmt, b_scaling, b_
     status = _L.fp8_scaled_gemm_ep(g, e, _stream(stream))
     if status:
         _check("fp8_scaled_gemm_ep", status)
+
+
+def fp8_gated_linear_workspace(M, F, K, a_scaling, b_scaling, backward=False) -> int:
+    """Bytes of workspace that fp8_gated_linear needs."""
+    return _L.fp8_gated_linear_workspace(M, F, K, a_scaling, b_scaling, 1 if backward else 0)
+
+
+def fp8_gated_linear(A, a_fmt, a_scaling, a_scale_inv, B, b_fmt, b_scaling, b_scale_inv, D, act=ACT_SILU, bias=None,
+                     aux=None, ck=None, ck_exp=None, backward=False, dbias=None, d_amax=None, stream=None, d_scale=None,
+                     d_fmt=None, D_t=None, amax_accumulate=False, workspace=None):
+    """The gated pair of a feed-forward block as one FP8 product.
+
+    Forward: A [M][K], B [2F][K] (the gate's rows, then the up projection's); g, u
+    = halves of A B^T + bias [2F]; D [M][F] = act(g) * u.  Backward: A [M][K] the
+    gradient of the next linear's output, B [F][K] that linear's weights; v = A B^T;
+    D [M][2F] = (v * u * act'(g) | v * act(g)), dbias [2F] its column sums.  D is
+    bf16, float32, or FP8 codes (uint8 or float8; d_fmt, d_scale, optional
+    transposed D_t).  g beside u are kept by the forward call, and read by the
+    backward one, as aux [M][2F] bf16 or as ck [M][2F] codes with ck_exp
+    [M][2 ceil(F / 32)] (see fp8_checkpoint_save).  All but the scales, biases and D_t
+    may have strided rows."""
+    M, K = A.shape
+    rows = B.shape[0]
+    if backward:
+        F, n = rows, 2 * rows
+    elif rows % 2:
+        raise ValueError(f"B must have the gate's rows and as many of the up projection, got {tuple(B.shape)}")
+    else:
+        F = n = rows // 2
+    mn = torch.Size((M, n))
+    dt = D.dtype
+    if dt in _U8:
+        if d_fmt not in (E4M3, E5M2):
+            raise ValueError("an FP8 output needs d_fmt (E4M3 or E5M2)")
+        d_dtype = OUT_E4M3 if d_fmt == E4M3 else OUT_E5M2
+    elif dt in _OUT:
+        d_dtype = _OUT[dt]
+    else:
+        raise TypeError(f"D has dtype {dt}, expected bf16, float32 or FP8 codes")
+    pt = _param_type(bias, dbias)
+    kept = torch.Size((M, 2 * F))
+    nkb = (K + 127) // 128 if M > 0 and F > 0 else 0
+    ap, lda = _codes(A, A.shape, "A")
+    bp, ldb = _codes(B, torch.Size((rows, K)), "B")
+    dp, ldd = _mat(D, mn, dt, "D")
+    tp, ldt = _codes(D_t, torch.Size((n, M)), "D_t") if D_t is not None else (0, M)
+    ws, wp, wn = _workspace(workspace, lambda: fp8_gated_linear_workspace(M, F, K, a_scaling, b_scaling, backward), A,
+                            stream)
+    g = _pack_gemm(M, F, K, lda, ldb, ldd, ap, a_fmt, a_scaling, _scales(a_scale_inv, a_scaling, M, nkb, "a_scale_inv"),
+                   bp, b_fmt, b_scaling, _scales(b_scale_inv, b_scaling, rows, nkb, "b_scale_inv"), dp, d_dtype,
+                   _floats(d_amax, 1, "d_amax"), 0, _floats(d_scale, 1, "d_scale"), tp, ldt,
+                   1 if amax_accumulate else 0)
+    e = _pack_gated(1 if backward else 0, act, _DT[pt], _vec(bias, 2 * F, pt, "bias"), *_mat(aux, kept, _BFLOAT, "aux"),
+                    *_codes(ck, kept, "ck"), *_bytes(ck_exp, torch.Size((M, 2 * ((F + 31) // 32))), "ck_exp"),
+                    _vec(dbias, 2 * F, pt, "dbias"), wp, wn)
+    status = _L.fp8_gated_linear(g, e, _stream(stream))
+    if status:
+        _check("fp8_gated_linear", status)
+
+
+def _bytes(t, shape, name):
+    """_mat of a checkpoint's powers of two (uint8 or float8_e8m0fnu)."""
+    if t is not None and t.dtype not in (torch.uint8, torch.float8_e8m0fnu):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected uint8 or float8_e8m0fnu")
+    return _mat(t, shape, None if t is None else t.dtype, name)
+
+
+def _checkpoint(x, ck, ck_exp, name):
+    rows, cols = shape = _two_dim(x, name)
+    if ck is None or ck_exp is None:
+        raise ValueError("ck and ck_exp are required")
+    return (rows, cols, *_mat(x, shape, x.dtype, name), *_codes(ck, shape, "ck"),
+            *_bytes(ck_exp, torch.Size((rows, (cols + 31) // 32)), "ck_exp"))
+
+
+def fp8_checkpoint_save(x, ck, ck_exp, stream=None):
+    """x [rows][cols], bf16 or float32, kept for the backward pass in 8 bits: ck
+    [rows][cols] E4M3 codes (uint8 or float8) and ck_exp [rows][ceil(cols / 32)] one
+    power of two for each 32 columns (uint8, or float8_e8m0fnu).  Rows may be strided."""
+    rows, cols, xp, ldx, cp, ldc, ep, lde = _checkpoint(x, ck, ck_exp, "x")
+    status = _L.fp8_checkpoint_save(xp, _DT[x.dtype], rows, cols, ldx, cp, ldc, ep, lde, _stream(stream))
+    if status:
+        _check("fp8_checkpoint_save", status)
+
+
+def fp8_checkpoint_load(ck, ck_exp, y, stream=None):
+    """y [rows][cols], bf16 or float32: the values of a checkpoint."""
+    rows, cols, yp, ldy, cp, ldc, ep, lde = _checkpoint(y, ck, ck_exp, "y")
+    status = _L.fp8_checkpoint_load(cp, ldc, ep, lde, rows, cols, yp, _DT[y.dtype], ldy, _stream(stream))
+    if status:
+        _check("fp8_checkpoint_load", status)
 
 
 def fp8_rope_freqs(freqs, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, trained=8192.0, low=1.0, high=32.0,

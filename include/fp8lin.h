@@ -483,6 +483,7 @@ fp8_status fp8_scaled_gemm(const fp8_gemm_args* args, hipStream_t stream);
  * a fixed order: equal inputs on equal hardware give equal bits.
  * ===================================================================== */
 #define FP8LIN_BLOCK_OPERATORS 1
+#define FP8LIN_GATED_OPERATORS 1   /* fp8_gated_linear, fp8_checkpoint_*: later still, the same way */
 typedef enum { FP8_DT_BF16 = 0, FP8_DT_F32 = 1 } fp8_dtype;
 typedef enum { FP8_NORM_RMS = 0, FP8_NORM_LAYER = 1 } fp8_norm_kind;
 /* Gate of a block's output: none, one value per channel [cols]
@@ -650,6 +651,85 @@ typedef struct {
 } fp8_ep_plan;
 
 fp8_status fp8_scaled_gemm_ep_plan(const fp8_gemm_args* gemm, const fp8_epilogue_args* ep, fp8_ep_plan* plan);
+
+/* ------------------------------------------------------------------------
+ * fp8_gated_linear -- the gated pair of a feed-forward block as one product.
+ * With F outputs per token (gemm->N = F) and every sum in binary32:
+ *   forward (backward = 0):  B holds 2 F rows, those of the gate's weights and
+ *     then those of the up projection's;  g[f] = A . B[f] + bias[f],
+ *     u[f] = A . B[F + f] + bias[F + f], dequantised as in fp8_scaled_gemm;
+ *     h = act(g) u, from the unrounded g and u;  D [M][F] = h.
+ *   backward (backward = 1):  B holds F rows (the next linear's weights, its
+ *     input dimension outermost);  v[f] = A . B[f], the gradient of h;
+ *     D [M][2 F] = (dg | du),  dg = v u act'(g),  du = v act(g);
+ *     dbias[2 F] = column sums of D before its rounding.
+ * D is BF16, FP32 or FP8 codes of d_scale times it (backward: one scale for
+ * both halves) with the transposed copy D_t ([F][ldt]; backward [2 F][ldt]);
+ * d_amax as in fp8_scaled_gemm.  With codes in both orders, D and D_t of a
+ * backward call are the operands of the products that follow, each one product
+ * over 2 F: the input's gradient (K = 2 F) and the weights' (2 F rows).
+ *   a_fmt     FP8_E4M3; backward also FP8_E5M2.   b_fmt  FP8_E4M3.
+ *   a_scaling, b_scaling  every combination of fp8_scaled_gemm; B's scales are
+ *             those of its rows, all 2 F of them forward.
+ *   act       as in fp8_scaled_gemm_ep (SiLU: SwiGLU, GELU: GEGLU, ReLU: ReGLU;
+ *             none: the product of the two).
+ *   bias [2 F], dbias [2 F]  param_dtype, optional.
+ *   What the backward call needs of the forward one, g beside u, in either form;
+ *   forward each is an optional output, backward one of them is the input:
+ *   aux       [M][ldaux] BF16, 2 F columns.
+ *   ck        [M][ldck] E4M3 codes, 2 F columns, and ck_exp [M][ldexp], 2 ceil(F /
+ *             32) bytes: g's and u's as fp8_checkpoint_save writes each.
+ *   workspace fp8_gated_linear_workspace(M, F, K, a_scaling, b_scaling, backward)
+ *             bytes.
+ * No output may overlap an input.  K == 0 is a sum of nothing; M == 0 sets dbias
+ * to 0.
+ * Errors: as fp8_scaled_gemm, and FP8_ERR_ARG (backward, act, param_dtype; a
+ * bias in a backward call, dbias in a forward one; aux and ck both in a backward
+ * one), FP8_ERR_NULL (one of ck and ck_exp alone; neither aux nor ck in a backward call;
+ * workspace), FP8_ERR_SHAPE (ldd of a backward call, ldaux, ldck < 2 F, ldexp < 2
+ * ceil(F / 32), a workspace that is too small), FP8_ERR_ALIGN,
+ * FP8_ERR_UNSUPPORTED (other formats; gemm's accumulate; 256 * lda or 256 * ldb >=
+ * 2^31; K > 65536; F > 2^26; more than 2^23 tiles of 128 x 128 of M x 2 F).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int backward;
+  fp8_activation act;
+  fp8_dtype param_dtype;
+  const void* bias;
+  void* aux; int64_t ldaux;
+  uint8_t* ck; int64_t ldck;
+  uint8_t* ck_exp; int64_t ldexp;
+  void* dbias;
+  void* workspace; int64_t workspace_bytes;
+} fp8_gated_args;
+
+int64_t fp8_gated_linear_workspace(int64_t M, int64_t F, int64_t K, fp8_scaling a_scaling, fp8_scaling b_scaling,
+                                   int backward);
+fp8_status fp8_gated_linear(const fp8_gemm_args* gemm, const fp8_gated_args* gated, hipStream_t stream);
+/* Which kernel the call takes (see fp8_scaled_gemm_ep_plan). */
+fp8_status fp8_gated_linear_plan(const fp8_gemm_args* gemm, const fp8_gated_args* gated, fp8_ep_plan* plan);
+
+/* ------------------------------------------------------------------------
+ * fp8_checkpoint_save, fp8_checkpoint_load -- a tensor that the backward pass
+ * needs, kept in 8 bits: E4M3 codes and one power of two for every 32 columns of
+ * a row (the last block of a row may be shorter), 8.25 bits a value.
+ * save:  with a = max |x| of the block and e the largest integer with a 2^e <= 448,
+ *   |e| <= 126 (0 for a block of zeros or one that holds an infinity or a NaN),
+ *   ck = encode(x 2^e) as in fp8_cast_e4m3, ck_exp = 127 - e.
+ * load:  y = value(ck) 2^(ck_exp - 127), rounded to nearest (exact in FP32 and, down
+ *   to its smallest normal value, in BF16); ck_exp is an E8M0 number (255: NaN).
+ *   x, y      [rows][ld] dtype.
+ *   ck        [rows][ldck] codes.   ck_exp [rows][ldexp], ceil(cols / 32) bytes.
+ * A value is kept to 2^-4 of itself, or to 2^-17 of its block's largest where that is
+ * more.  save's outputs may not overlap x, load's not ck or ck_exp.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (negative size, ld < cols, ldexp < ceil(cols /
+ * 32)), FP8_ERR_ARG (dtype), FP8_ERR_ALIGN (x, y: their element), FP8_ERR_UNSUPPORTED
+ * (cols > 2^28).
+ * ---------------------------------------------------------------------- */
+fp8_status fp8_checkpoint_save(const void* x, fp8_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, uint8_t* ck,
+                               int64_t ldck, uint8_t* ck_exp, int64_t ldexp, hipStream_t stream);
+fp8_status fp8_checkpoint_load(const uint8_t* ck, int64_t ldck, const uint8_t* ck_exp, int64_t ldexp, int64_t rows,
+                               int64_t cols, void* y, fp8_dtype dtype, int64_t ldy, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * fp8_rope -- rotary positions of the query and key heads of a QKV product.
