@@ -311,6 +311,13 @@ __device__ __forceinline__ v4f mfma(const v8i& a, const v8i& b, const v4f& c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, AF, BF, 0, 0, 0, 0);
 }
 
+// Columns of a product with two factors: 16 of the one, the same 16 of the other, and so
+// on.  Which factor and which of its columns column c stands for, and how many columns
+// n pairs take (a multiple of 32).
+__host__ __device__ constexpr int half_of(int c) { return (c >> 4) & 1; }
+__host__ __device__ constexpr int pair_of(int c) { return 16 * (c >> 5) + (c & 15); }
+__host__ __device__ constexpr int64_t paired_columns(int64_t n) { return (n + 15) / 16 * 32; }
+
 // max(a, b, c) of unsigned words as one instruction that the compiler keeps
 // where it stands (volatile asm): an unsigned maximum over |x| bit patterns
 // is the amax of binary32 values, NaN above +Inf.

@@ -427,13 +427,21 @@ __device__ __forceinline__ void workgroup_amax(float* d_amax, uint32_t amax_bits
 // SB_COL : B has 1x128 scales (one per column and K block), else one per wave;
 // MX     : always false here.
 // EP     : the linear's epilogue (gemm_ep.h) in place of the plain one, its
-//          arguments in `ep` (NoEpilogue: none).
-struct NoEpilogue {};
+//          arguments in `ep` (NoEpilogue: none).  A PAIRED one's B has 2 N rows,
+//          N of each of two factors, and a tile's 256 columns are 16 of the one,
+//          16 of the other and so on (half_of, pair_of): 128 pairs.  B's scales
+//          are 128 x 128 blocks and N a multiple of 128, so that a tile has one
+//          scale for each factor.
+struct NoEpilogue {
+  static constexpr bool PAIRED = false;
+};
 template <int AF, int BF, bool BLOCK, bool SA_ROWS, bool SB_COL, bool MX, bool OUT8, typename EP = NoEpilogue>
 __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   static_assert(BLOCK && !MX, "per-tensor, per-row and power-of-two scales run on k_gemm_w4");
+  constexpr bool PAIRED = EP::PAIRED;
+  static_assert(!PAIRED || (SA_ROWS && !SB_COL), "pairs: rows of A, blocks of B");
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE];
-  __shared__ float su_tab[NWAVES][MAX_KB];
+  __shared__ float su_tab[PAIRED ? 2 : NWAVES][MAX_KB];   // (PAIRED: of each factor)
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -450,11 +458,13 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
   const int gm = min(tiles_m - first_m, GROUP_M);
   const int in_group = bid - group * GROUP_M * tiles_n;
   const int tm = first_m + in_group % gm, tn = in_group / gm;
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  constexpr int BNP = PAIRED ? BN / 2 : BN;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BNP;
 
-  const int64_t rows_a = min((int64_t)BM, M - m0), rows_b = min((int64_t)BN, N - n0);
+  const int64_t rows_a = min((int64_t)BM, M - m0), rows_b = min((int64_t)BNP, N - n0);
   const i32x4 ra = make_rsrc(p.A + m0 * p.lda, (uint32_t)(rows_a * p.lda));
   const i32x4 rb = make_rsrc(p.B + n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
+  const i32x4 rb2 = PAIRED ? make_rsrc(p.B + (N + n0) * p.ldb, (uint32_t)(rows_b * p.ldb)) : rb;
   const int lda = (int)p.lda, ldb = (int)p.ldb;
   // DMA: wave w fills rows 32w .. 32w+31 of A and of B, 8 rows per
   // instruction; lane p lands in row 8*it + (p >> 3), stored chunk p & 7
@@ -474,8 +484,8 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
     if (q < 4)
       dma16s(lb + (32 * wave + 8 * it) * BK, (uint32_t)(row * lda + kc), ra, (uint32_t)(kb * BK));
     else
-      dma16s(lb + A_BYTES + (32 * wave + 8 * it) * BK, (uint32_t)(row * ldb + kc), rb,
-             (uint32_t)(kb * BK));
+      dma16s(lb + A_BYTES + (32 * wave + 8 * it) * BK, (uint32_t)((PAIRED ? pair_of(row) : row) * ldb + kc),
+             PAIRED && half_of(8 * it) ? rb2 : rb, (uint32_t)(kb * BK));
   };
   auto load_scales = [&](int kb, uint8_t* base) {
     const uint32_t lb = lds_addr(base);
@@ -518,7 +528,13 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
   if (nk > 1) load_stage(1, lds[1]);
 
   // ---- per-wavefront table of the uniform part of each K block's scale
-  if constexpr (!(SA_ROWS && SB_COL)) {
+  if constexpr (PAIRED) {
+    const int64_t nb = n0 / 128, all = (2 * N + 127) / 128;
+    for (int i = tid; i < 2 * nk; i += THREADS) {
+      const int h = i >= nk ? 1 : 0, kb = h ? i - nk : i;
+      su_tab[h][kb] = p.b_scaling == 0 ? p.b_sinv[0] : p.b_sinv[kb * all + nb + (h ? N / 128 : 0)];
+    }
+  } else if constexpr (!(SA_ROWS && SB_COL)) {
     const int64_t mb = min((m0 + wm * WTM) / 128, (M + 127) / 128 - 1);
     const int64_t nb = min((n0 + wn * WTN) / 128, (N + 127) / 128 - 1);
     for (int kb = lane; kb < nk; kb += 64) {
@@ -573,14 +589,19 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
           scol[j][0] = sv.x; scol[j][1] = sv.y; scol[j][2] = sv.z; scol[j][3] = sv.w;
         }
       }
-      float suni = 1.0f;
-      if constexpr (!(SA_ROWS && SB_COL)) suni = su_tab[wave][kb];
+      float suni = 1.0f, suni2 = 1.0f;
+      if constexpr (PAIRED) {
+        suni = su_tab[0][kb];
+        suni2 = su_tab[1][kb];
+      } else if constexpr (!(SA_ROWS && SB_COL)) {
+        suni = su_tab[wave][kb];
+      }
       // one row-tile at a time: the next A fragment is read while this
       // tile's MFMAs run, and the block partials of the previous row-tile
       // are promoted while this row's MFMAs execute (their results are
       // long ready by then); the last row is promoted after the loop.  The
       // scheduling barrier keeps each row's MFMAs ahead of the promotion.
-      auto promote = [&](int i, const v4f (&pp)[TJ], float sr) {
+      auto promote = [&](int i, const v4f (&pp)[TJ], float sr, float sr2) {
 #pragma unroll
         for (int j = 0; j < TJ; ++j)
 #pragma unroll
@@ -588,19 +609,20 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
             if constexpr (SB_COL)
               acc[i][j][r] = __builtin_fmaf(pp[j][r] * sr, scol[j][r], acc[i][j][r]);
             else
-              acc[i][j][r] = __builtin_fmaf(pp[j][r], sr, acc[i][j][r]);
+              acc[i][j][r] = __builtin_fmaf(pp[j][r], PAIRED && (j & 1) ? sr2 : sr, acc[i][j][r]);
           }
       };
       v8i a_cur = a_first;
       v4f pprev[TJ];
-      float sprev = 0.0f;
+      float sprev = 0.0f, sprev2 = 0.0f;
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
         v8i a_nxt = a_cur;
         if (i + 1 < TI) a_nxt = frag(As, wm * WTM + 16 * (i + 1) + l16, g);
-        float srow = suni;
+        float srow = suni, srow2 = 1.0f;
         if constexpr (SA_ROWS) {
           srow = reinterpret_cast<const float*>(As + SA_OFF)[wm * WTM + 16 * i + l16];
+          if constexpr (PAIRED) srow2 = srow * suni2;
           if constexpr (!SB_COL) srow *= suni;
         }
         // the next stage's operand DMA, PER instructions with each of the
@@ -615,10 +637,11 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
         v4f pcur[TJ];
 #pragma unroll
         for (int j = 0; j < TJ; ++j) pcur[j] = mfma<BF, AF>(bfr[j], a_cur, v4f{0.f, 0.f, 0.f, 0.f});
-        if (i > 0) promote(i - 1, pprev, sprev);
+        if (i > 0) promote(i - 1, pprev, sprev, sprev2);
 #pragma unroll
         for (int j = 0; j < TJ; ++j) pprev[j] = pcur[j];
         sprev = srow;
+        sprev2 = srow2;
         a_cur = a_nxt;
         // one matrix instruction, then its share of the promotion
 #pragma unroll
@@ -628,7 +651,7 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      promote(TI - 1, pprev, sprev);
+      promote(TI - 1, pprev, sprev, sprev2);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
@@ -649,8 +672,8 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
   auto deq = [&](int, int, int, float a) -> float { return a; };
   if constexpr (!std::is_same_v<EP, NoEpilogue>) {
     __syncthreads();   // every wavefront is done reading both stages
-    ep.template finish<OUT8, TI, TJ, NWAVES>(p, acc, deq, m0 + wm * WTM, n0 + wn * WTN, tm * 2 + wm, lane, wave,
-                                             &lds[0][0] + wave * 16384);
+    ep.template finish<OUT8, TI, TJ, NWAVES>(p, acc, deq, m0 + wm * WTM, (int64_t)tn * BN + wn * WTN, tm * 2 + wm, lane,
+                                             wave, &lds[0][0] + wave * 16384);
     return;
   }
   const int esz = OUT8 ? 1 : (p.d_f32 ? 4 : 2);

@@ -435,16 +435,9 @@ struct EpWave {
 template <int NW>
 __device__ __forceinline__ void ep_amax(float* d_amax, uint32_t bits, int lane, int wave);
 
-// Columns of a product with two factors: 16 of the one, the same 16 of the other, and so
-// on.  Which factor and which of its columns column c stands for, and how many columns
-// n pairs take (a multiple of 32).
-__host__ __device__ constexpr int half_of(int c) { return (c >> 4) & 1; }
-__host__ __device__ constexpr int pair_of(int c) { return 16 * (c >> 5) + (c & 15); }
-__host__ __device__ constexpr int64_t paired_columns(int64_t n) { return (n + 15) / 16 * 32; }
-
 // What the kernels on tiles and on few rows are built around: the epilogue's
 // arguments, and who takes a wavefront's sums of WTN columns of B's rows.  PAIRED: B's
-// rows come in pairs of a product with two factors (gemm_gated.h).
+// rows come in pairs of a product with two factors (see half_of in fp8_device.h).
 struct LinearOp {
   using Params = EpParams;
   static constexpr bool PAIRED = false;

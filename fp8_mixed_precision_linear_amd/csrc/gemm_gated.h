@@ -11,7 +11,7 @@
 //
 // Forward the two factors of an output have to meet in one lane.  So B's rows are taken
 // 16 of the gate, the same 16 of the up projection, and so on (half_of, pair_of in
-// gemm_ep.h): the matrix instruction's column tiles alternate, and a strip of 16 rows in
+// fp8_device.h): the matrix instruction's column tiles alternate, and a strip of 16 rows in
 // LDS (see gemm_ep.h) holds both factors of the outputs.  A lane reads eight of each.
 // The checkpoint's blocks are 32 outputs of a row, four neighbouring lanes: no exchange
 // beyond a quad, and none between wavefronts.
@@ -491,6 +491,36 @@ struct GatedGradOp {
   static constexpr bool PAIRED = false;
   template <int WTN, bool OUT8>
   using Wave = GatedGradWave<WTN, OUT8, false, 2>;
+};
+
+// The epilogue as the large kernels take it (see LinearEp).
+template <typename W, int TI, int TJ, int NW, typename Deq>
+__device__ __forceinline__ void gated_finish(const GemmParams& p, const GatedParams& e, const v4f (&acc)[TI][TJ], Deq&& deq,
+                                             int64_t r0, int64_t c0, int64_t part, int lane, int wave, uint8_t* wl) {
+  static_assert(W::bytes(TI) <= 128 * 1024 / NW, "the wavefront's part of the stages");
+  W w(p, e, c0, lane);
+  w.template tile<TI, TJ>(acc, deq, r0, c0, wl);
+  w.put_dbias(part);
+  if (p.d_amax) ep_amax<NW>(p.d_amax, w.amax_bits(), lane, wave);
+}
+struct GatedEp {
+  static constexpr bool PAIRED = true;
+  GatedParams e;
+  template <bool OUT8, int TI, int TJ, int NW, typename Deq>
+  __device__ __forceinline__ void finish(const GemmParams& p, const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t c0,
+                                         int64_t part, int lane, int wave, uint8_t* wl) const {
+    gated_finish<GatedWave<16 * TJ, OUT8, true>, TI, TJ, NW>(p, e, acc, deq, r0, c0, part, lane, wave, wl);
+  }
+};
+template <int KEPT>
+struct GatedGradEp {
+  static constexpr bool PAIRED = false;
+  GatedParams e;
+  template <bool OUT8, int TI, int TJ, int NW, typename Deq>
+  __device__ __forceinline__ void finish(const GemmParams& p, const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t c0,
+                                         int64_t part, int lane, int wave, uint8_t* wl) const {
+    gated_finish<GatedGradWave<16 * TJ, OUT8, true, KEPT>, TI, TJ, NW>(p, e, acc, deq, r0, c0, part, lane, wave, wl);
+  }
 };
 
 }  // namespace

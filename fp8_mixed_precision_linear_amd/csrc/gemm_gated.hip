@@ -64,8 +64,8 @@ EpPlan plan_of(const GemmParams& p, int backward, bool tiles) {
   if (!backward) v.N = paired_columns(p.N);
   if (tiles && v.M > 0 && v.M <= 16) v.M = 17;
   EpPlan plan = ep_plan(v);
-  plan.large = false;
-  plan.part_bytes = backward ? (plan.parts * 2 * p.N * 4 + 255) / 256 * 256 : 0;
+  const int64_t parts = plan.parts > plan.large_parts ? plan.parts : plan.large_parts;   // (either may be taken)
+  plan.part_bytes = backward ? (parts * 2 * p.N * 4 + 255) / 256 * 256 : 0;
   plan.sums_bytes = plan.splits > 1 ? plan.splits * p.M * plan.ldw * 4 : 0;
   return plan;
 }
@@ -76,8 +76,23 @@ EpPlan plan_of(const GemmParams& p, int backward, bool tiles) {
 // the tiles (the few-row kernel's 16 outputs are half a block), and for one that does not.
 EpPlan gated_plan(const GemmParams& p, int backward) { return plan_of(p, backward, !backward); }
 
+namespace {
+// What the large kernels take: see gemm_gated_large.h.
+bool large_takes(const GemmParams& p, const GatedParams& e) {
+  auto dwords = [](const void* q, int64_t ld, int size) {
+    return q == nullptr || (((reinterpret_cast<uintptr_t>(q) & 3u) == 0) && ((ld * size) & 3) == 0);
+  };
+  const bool blocks = p.a_scaling != 0 && p.a_scaling != 5;
+  return p.N % (blocks && !e.backward ? 128 : 8) == 0 && dwords(p.D, p.ldd, p.d_fp8 ? 1 : (p.d_f32 ? 4 : 2)) &&
+         dwords(e.aux, e.ldaux, 2) && dwords(e.ck, e.ldck, 1);
+}
+}  // namespace
+
 EpPlan gated_plan(const GemmParams& p, const GatedParams& e) {
-  return plan_of(p, e.backward, !e.backward && e.ck != nullptr);
+  EpPlan plan = plan_of(p, e.backward, !e.backward && e.ck != nullptr);
+  plan.large = plan.large && large_takes(p, e);
+  if (plan.large) plan.splits = 1;
+  return plan;
 }
 
 hipError_t launch_gated(const GemmParams& p0, GatedParams e, uint8_t* ws, hipStream_t s) {
@@ -94,6 +109,12 @@ hipError_t launch_gated(const GemmParams& p0, GatedParams e, uint8_t* ws, hipStr
   e.splits = plan.splits;
   // (powers of two on every block-scaled operand go into the matrix instruction; beside
   // others, and for few rows, they are binary32 scales of the same layouts)
+  if (plan.large) {
+    const hipError_t err = !e.backward ? launch_gated_large(p, e, s)
+                           : p.a_fmt == 0 ? launch_gated_grad_large(p, e, s) : launch_gated_grad_large_e5m2(p, e, s);
+    if (err != hipSuccess) return err;
+    return e.dbias ? launch_ep_dbias(e.part, plan.large_parts, 2 * p.N, e.dbias, e.bias_f32, s) : hipSuccess;
+  }
   const bool promoted = p.a_scaling == 1 || p.a_scaling == 2 || p.b_scaling == 1 || p.b_scaling == 2;
   if (p.a_scaling == 3 || p.a_scaling == 4) p.a_scaling -= 2;
   if (p.b_scaling == 3 || p.b_scaling == 4) p.b_scaling -= 2;

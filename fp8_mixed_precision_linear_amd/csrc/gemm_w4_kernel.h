@@ -59,20 +59,24 @@ constexpr int W4_OUT8_PASSES = 2;
 // FP8 training recipe in detail > Block-wise scaling at 128 granularity";
 // a per-tensor operand's scale goes to the epilogue).
 // EP: the linear's epilogue (gemm_ep.h) in place of the plain one, its arguments
-// in `ep` (NoEpilogue: none).
+// in `ep` (NoEpilogue: none).  A PAIRED one's columns are pairs of B's rows (see
+// k_gemm_big; N a multiple of 128 in the block modes, of 1 in the others).
 template <int AF, int BF, bool KT, bool OUT8, int MODE, typename EP = NoEpilogue>
 __global__ void __launch_bounds__(W4_THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
 k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   constexpr bool ROWS = MODE == W4_ROWS, MX = MODE >= W4_MX;
   constexpr bool SA_ROWS = MX && ((MODE - W4_MX) & 1), SB_COL = MX && ((MODE - W4_MX) & 2);
+  constexpr bool PAIRED = EP::PAIRED;
   static_assert(!(MX && KT), "block scales make K a multiple of the step");
+  static_assert(!(PAIRED && SB_COL), "pairs: blocks of B");
   // a stage: A, B, then (block modes) 256 row scales of A and of B
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][MX ? STAGE : W4_STAGE];
   // per-row scales of the tile's 256 D rows and 256 D columns (rows clamped
   // into D for edge tiles), read in the epilogue
   __shared__ float rs_tab[ROWS ? BM + BN : 1];
   // block modes: per wavefront and K block, the E8M0 codes of the uniform
-  // (128 x 128 or per-tensor) scales, A in bits 0-7, B in bits 8-15
+  // (128 x 128 or per-tensor) scales, A in bits 0-7, B in bits 8-15 (PAIRED: B's
+  // second factor in bits 16-23)
   __shared__ float su_tab[MX ? 4 : 1][MX ? MAX_KB : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -90,11 +94,13 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   const int gm = min(tiles_m - first_m, GROUP_M);
   const int in_group = bid - group * GROUP_M * tiles_n;
   const int tm = first_m + in_group % gm, tn = in_group / gm;
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  constexpr int BNP = PAIRED ? BN / 2 : BN;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BNP;
 
-  const int64_t rows_a = min((int64_t)BM, M - m0), rows_b = min((int64_t)BN, N - n0);
+  const int64_t rows_a = min((int64_t)BM, M - m0), rows_b = min((int64_t)BNP, N - n0);
   const i32x4 ra = make_rsrc(p.A + m0 * p.lda, (uint32_t)(rows_a * p.lda));
   const i32x4 rb = make_rsrc(p.B + n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
+  const i32x4 rb2 = PAIRED ? make_rsrc(p.B + (N + n0) * p.ldb, (uint32_t)(rows_b * p.ldb)) : rb;
   const int lda = (int)p.lda, ldb = (int)p.ldb;
 
   // the epilogue's scales, read ahead of the first DMA (its wait covers them)
@@ -123,7 +129,7 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   for (int it = 0; it < 8; ++it) {
     const int row = 64 * wave + 8 * it + (lane >> 3);
     ro[0][it] = (uint32_t)(row * lda);
-    ro[1][it] = (uint32_t)(row * ldb);
+    ro[1][it] = (uint32_t)((PAIRED ? pair_of(row) : row) * ldb);
   }
 #pragma unroll
   for (int par = 0; par < 2; ++par)
@@ -131,11 +137,12 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   auto load = [&](int kb, const uint8_t* base, int q) {   // q: 0..7 A, 8..15 B
     const int o = q >> 3, it = q & 7;
     const uint32_t dst = lds_addr(base) + (o ? A_BYTES : 0) + (64 * wave + 8 * it) * BK;
+    const i32x4& rs = o ? (PAIRED && half_of(8 * it) ? rb2 : rb) : ra;
     if constexpr (!KT) {
-      dma16s(dst, ro[o][it] + kcl[it & 1], o ? rb : ra, (uint32_t)(kb * BK));
+      dma16s(dst, ro[o][it] + kcl[it & 1], rs, (uint32_t)(kb * BK));
     } else {
       const int kc = kb * BK + (int)kcl[it & 1];
-      dma16(dst, kc < (int)K ? ro[o][it] + (uint32_t)kc : kOOB, o ? rb : ra);
+      dma16(dst, kc < (int)K ? ro[o][it] + (uint32_t)kc : kOOB, rs);
     }
   };
   // block modes: the K block's 256 A row scales and 256 B column scales,
@@ -172,23 +179,26 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   if constexpr (ROWS) {   // thread t: A's scale of D row m0 + t, then B's of column n0 + t
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t r = (h == 0 ? m0 : n0) + tid, lim = h == 0 ? M : N;
+      const int64_t r = (h == 0 ? m0 : n0) + (PAIRED && h ? pair_of(tid) : tid), lim = h == 0 ? M : N;
       const bool row_mode = (h == 0 ? p.a_scaling : p.b_scaling) == 5;
-      rs_tab[h * BM + tid] = (h == 0 ? p.a_sinv : p.b_sinv)[row_mode ? (r < lim ? r : lim - 1) : 0];
+      const int64_t row = (r < lim ? r : lim - 1) + (PAIRED && h && half_of(tid) ? N : 0);
+      rs_tab[h * BM + tid] = (h == 0 ? p.a_sinv : p.b_sinv)[row_mode ? row : 0];
     }
   }
   if constexpr (MX && !(SA_ROWS && SB_COL)) {
     // the uniform parts: the wavefront's 128 rows and 128 columns each sit
     // in one 128 x 128 block (1.0, code 127, for a per-tensor operand)
     const int64_t mb = min((m0 + wm * 128) / 128, (M + 127) / 128 - 1);
-    const int64_t nb = min((n0 + wn * 128) / 128, (N + 127) / 128 - 1);
+    const int64_t nb = PAIRED ? n0 / 128 : min((n0 + wn * 128) / 128, (N + 127) / 128 - 1);
+    const int64_t all = ((PAIRED ? 2 * N : N) + 127) / 128;
     for (int k = lane; k < nk; k += 64) {
-      int ea = 127, eb = 127;
+      int ea = 127, eb = 127, eb2 = 0;
       if constexpr (!SA_ROWS)
         if (p.a_scaling != 0) ea = e8m0_of(p.a_sinv[k * ((M + 127) / 128) + mb]);
       if constexpr (!SB_COL)
-        if (p.b_scaling != 0) eb = e8m0_of(p.b_sinv[k * ((N + 127) / 128) + nb]);
-      su_tab[wave][k] = __uint_as_float((uint32_t)ea | ((uint32_t)eb << 8));
+        if (p.b_scaling != 0) eb = e8m0_of(p.b_sinv[k * all + nb]);
+      if constexpr (PAIRED) eb2 = p.b_scaling != 0 ? e8m0_of(p.b_sinv[k * all + nb + N / 128]) : 127;
+      su_tab[wave][k] = __uint_as_float((uint32_t)ea | ((uint32_t)eb << 8) | ((uint32_t)eb2 << 16));
     }
   }
   // stage 0 done (in the block modes up to 2 more DMA instructions per
@@ -225,7 +235,7 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   // one MFMA: plain, or with the block codes of row-tile i and column-tile j
   auto mm = [&](const v8i& bj, const v8i& ai, const v4f& c, int i, int j, uint32_t eu) -> v4f {
     if constexpr (MX)
-      return mfma_mx<BF, AF>(bj, ai, c, SB_COL ? e8m0_of(eb[j]) : (int)((eu >> 8) & 0xFFu),
+      return mfma_mx<BF, AF>(bj, ai, c, SB_COL ? e8m0_of(eb[j]) : (int)((eu >> (PAIRED && (j & 1) ? 16 : 8)) & 0xFFu),
                              SA_ROWS ? e8m0_of(ea[i]) : (int)(eu & 0xFFu));
     else
       return mfma<BF, AF>(bj, ai, c);
@@ -322,7 +332,7 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   };
   if constexpr (!std::is_same_v<EP, NoEpilogue>) {
     __syncthreads();   // every wavefront is done reading both stages
-    ep.template finish<OUT8, 8, 8, 4>(p, acc, deq, m0 + wm * 128, n0 + wn * 128, tm * 2 + wm, lane, wave,
+    ep.template finish<OUT8, 8, 8, 4>(p, acc, deq, m0 + wm * 128, (int64_t)tn * BN + wn * 128, tm * 2 + wm, lane, wave,
                                       &lds[0][0] + wave * 32768);
     return;
   }

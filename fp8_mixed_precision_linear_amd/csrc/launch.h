@@ -243,6 +243,10 @@ hipError_t launch_gated_tile(const GemmParams& p, const GatedParams& e, const Ep
 hipError_t launch_gated_tile_blk(const GemmParams& p, const GatedParams& e, const EpPlan& plan, hipStream_t s);
 hipError_t launch_gated_grad_tile(const GemmParams& p, const GatedParams& e, const EpPlan& plan, hipStream_t s);
 hipError_t launch_gated_grad_tile_blk(const GemmParams& p, const GatedParams& e, const EpPlan& plan, hipStream_t s);
+// (power-of-two scalings keep their codes, as in launch_gemm_ep_large)
+hipError_t launch_gated_large(const GemmParams& p, const GatedParams& e, hipStream_t s);
+hipError_t launch_gated_grad_large(const GemmParams& p, const GatedParams& e, hipStream_t s);
+hipError_t launch_gated_grad_large_e5m2(const GemmParams& p, const GatedParams& e, hipStream_t s);
 hipError_t launch_gated_skinny(const GemmParams& p, const GatedParams& e, hipStream_t s);
 
 // 8-bit checkpoints (checkpoint_kernels.hip).
