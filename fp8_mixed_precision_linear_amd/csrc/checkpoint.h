@@ -24,21 +24,47 @@ __device__ __forceinline__ uint32_t ck_exponent(uint32_t amax) {
   const int b = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return amax == 0u || amax >= 0x7F800000u ? 127u : (uint32_t)(b < 1 ? 1 : b);
 }
-// 2^e, and back: 2^-e.  (Bytes are 1 .. 247 as made here; read, 0 is 2^-127, a binary32
-// subnormal, and 255 a NaN, as E8M0 has them.)
+// 2^e.
 __device__ __forceinline__ float ck_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
-__device__ __forceinline__ float ck_unscale(uint32_t byte) {
-  return __uint_as_float(byte == 255u ? 0x7FC00000u : (byte == 0u ? 0x00400000u : byte << 23));
+
+// Eight values of a block without infinities or NaN as codes: the conversion divides by
+// 2^(byte - 127), given as a binary32 of which it takes the exponent.
+typedef short ck_s2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void ck_codes(const float (&v)[8], uint32_t byte, uint32_t& lo, uint32_t& hi) {
+  const float s = __uint_as_float(byte << 23);
+  ck_s2 a = {0, 0}, b = {0, 0};
+  a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(a, v[0], v[1], s, false);
+  a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(a, v[2], v[3], s, true);
+  b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[4], v[5], s, false);
+  b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[6], v[7], s, true);
+  lo = __builtin_bit_cast(uint32_t, a);
+  hi = __builtin_bit_cast(uint32_t, b);
+}
+// Four and eight values from their codes and the block's byte.
+__device__ __forceinline__ void ck_values(uint32_t w, uint32_t byte, float (&v)[4]) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const float s = __uint_as_float(byte << 23);
+  const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, false), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, true);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+__device__ __forceinline__ void ck_values(uint32_t lo, uint32_t hi, uint32_t byte, float (&v)[8]) {
+  float a[4], b[4];
+  ck_values(lo, byte, a);
+  ck_values(hi, byte, b);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[k] = a[k];
+    v[k + 4] = b[k];
+  }
 }
 
-// Eight values from their codes and the block's byte.
-__device__ __forceinline__ void ck_values(uint32_t lo, uint32_t hi, uint32_t byte, float (&v)[8]) {
-  const float s = ck_unscale(byte);
-  typedef float f2 __attribute__((ext_vector_type(2)));
-  const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, true);
-  const f2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, false), d = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, true);
-  v[0] = a.x * s; v[1] = a.y * s; v[2] = b.x * s; v[3] = b.y * s;
-  v[4] = c.x * s; v[5] = c.y * s; v[6] = d.x * s; v[7] = d.y * s;
+// max |v| of eight; a NaN among them is the maximum.
+__device__ __forceinline__ float max8(const float (&v)[8]) {
+  float m = __builtin_elementwise_maximum(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
+#pragma unroll
+  for (int k = 2; k < 8; k += 2)
+    m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, __builtin_fabsf(v[k])), __builtin_fabsf(v[k + 1]));
+  return m;
 }
 
 }  // namespace

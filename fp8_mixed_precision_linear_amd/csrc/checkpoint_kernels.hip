@@ -35,13 +35,18 @@ __global__ void __launch_bounds__(CK_THREADS) k_checkpoint_save(const void* x, i
     uint32_t a = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) a = max_u32(a, abs_bits(v[k]));
+    const bool tame = __builtin_amdgcn_ballot_w64(a >= 0x7F800000u) == 0;
     a = max_u32(a, dpp<kXor1>(a));
     a = max_u32(a, dpp<kXor2>(a));
     const uint32_t byte = ck_exponent(a);
     uint32_t lo, hi;
+    if (__builtin_expect(tame, 1)) {
+      ck_codes(v, byte, lo, hi);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= ck_scale(byte);
-    codes8(0, v, 1.0f, lo, hi);
+      for (int k = 0; k < 8; ++k) v[k] *= ck_scale(byte);
+      codes8(0, v, 1.0f, lo, hi);
+    }
     store_codes(ck + r * ldck + c, n, lo, hi);
     if ((threadIdx.x & 3) == 0 && n > 0) ck_exp[r * ldexp + (c >> 5)] = (uint8_t)byte;
   }

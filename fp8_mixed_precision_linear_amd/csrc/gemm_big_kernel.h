@@ -431,14 +431,15 @@ __device__ __forceinline__ void workgroup_amax(float* d_amax, uint32_t amax_bits
 //          N of each of two factors, and a tile's 256 columns are 16 of the one,
 //          16 of the other and so on (half_of, pair_of): 128 pairs.  B's scales
 //          are 128 x 128 blocks and N a multiple of 128, so that a tile has one
-//          scale for each factor.
+//          scale for each factor.  (DIRECT: see k_gemm_w4.)
 struct NoEpilogue {
-  static constexpr bool PAIRED = false;
+  static constexpr bool PAIRED = false, DIRECT = false;
 };
 template <int AF, int BF, bool BLOCK, bool SA_ROWS, bool SB_COL, bool MX, bool OUT8, typename EP = NoEpilogue>
 __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   static_assert(BLOCK && !MX, "per-tensor, per-row and power-of-two scales run on k_gemm_w4");
   constexpr bool PAIRED = EP::PAIRED;
+  static_assert(!EP::DIRECT, "k_gemm_w4's");
   static_assert(!PAIRED || (SA_ROWS && !SB_COL), "pairs: rows of A, blocks of B");
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE];
   __shared__ float su_tab[PAIRED ? 2 : NWAVES][MAX_KB];   // (PAIRED: of each factor)

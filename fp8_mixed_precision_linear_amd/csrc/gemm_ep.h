@@ -449,7 +449,7 @@ struct LinearOp {
 // rows start at r0 and columns at c0; part: its row of column sums.
 template <int DIR>
 struct LinearEp {
-  static constexpr bool PAIRED = false;
+  static constexpr bool PAIRED = false, DIRECT = false;
   EpParams e;
   template <bool OUT8, int TI, int TJ, int NW, typename Deq>
   __device__ __forceinline__ void finish(const GemmParams& p, const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0,

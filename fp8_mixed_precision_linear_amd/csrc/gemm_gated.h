@@ -24,34 +24,74 @@ namespace fp8lin {
 
 namespace {
 
-// act(u) and act'(u), which share their exponential and reciprocal.
-__device__ __forceinline__ void act_and_slope(int act, const float (&u)[8], float (&a)[8], float (&s)[8]) {
-  if (act >= 3) {
+// act(u), and act(u) beside act'(u), which share their exponential and reciprocal.  A
+// uniform run-time choice per eight values.  SiLU, with s = 1 / (1 + e^-u), has the
+// slope s + u s (1 - s).
+__device__ __forceinline__ void act_of(int act, const float (&u)[8], float (&a)[8]) {
+  if (act == 4) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = u[k] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * u[k]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = u[k];
+    activate<false>(act, a, u);
+  }
+}
+template <int E>
+__device__ __forceinline__ void act_and_slope(int act, const float (&u)[E], float (&a)[E], float (&s)[E]) {
+  if (act == 4) {
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const float g = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * u[k]));
+      a[k] = u[k] * g;
+      s[k] = __builtin_fmaf(a[k], 1.0f - g, g);
+    }
+  } else if (act == 3) {
     const SigmoidForm f(act);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f.both(u[k], a[k], s[k]);
+    for (int k = 0; k < E; ++k) f.both(u[k], a[k], s[k]);
   } else if (act == 2) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < E; ++k) {
       a[k] = gelu_erf<false>(u[k]);
       s[k] = gelu_erf<true>(u[k]);
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < E; ++k) {
       a[k] = act == 1 && u[k] <= 0.0f ? 0.0f : u[k];
       s[k] = act == 1 && !(u[k] > 0.0f) ? 0.0f : 1.0f;
     }
   }
 }
 
-// Eight values as FP8 codes of v * so.
-__device__ __forceinline__ void codes_of(int fp8, const float (&v)[8], float so, uint32_t& lo, uint32_t& hi) {
-  float x[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = v[k] * so;
-  if (fp8 == 1) encode8<0>(x, lo, hi);
-  else encode8<1>(x, lo, hi);
+// Eight values x as FP8 codes.  `tame`: none of them is a NaN or beyond the format's
+// largest, so they need neither saturation nor a patch (a third of the instructions).
+template <int FMT>
+__device__ __forceinline__ void encode_tame(const float (&x)[8], uint32_t& lo, uint32_t& hi) {
+  int a, b;
+  if constexpr (FMT == 0) {
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], a, true);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], b, true);
+  } else {
+    a = __builtin_amdgcn_cvt_pk_bf8_f32(x[0], x[1], 0, false);
+    a = __builtin_amdgcn_cvt_pk_bf8_f32(x[2], x[3], a, true);
+    b = __builtin_amdgcn_cvt_pk_bf8_f32(x[4], x[5], 0, false);
+    b = __builtin_amdgcn_cvt_pk_bf8_f32(x[6], x[7], b, true);
+  }
+  lo = (uint32_t)a;
+  hi = (uint32_t)b;
+}
+__device__ __forceinline__ void codes_of(int fp8, bool tame, const float (&x)[8], uint32_t& lo, uint32_t& hi) {
+  if (fp8 == 1) {
+    if (__builtin_expect(tame, 1)) encode_tame<0>(x, lo, hi);
+    else encode8<0>(x, lo, hi);
+  } else {
+    if (__builtin_expect(tame, 1)) encode_tame<1>(x, lo, hi);
+    else encode8<1>(x, lo, hi);
+  }
 }
 // Code k to the top of column k's word, the rows before down a byte.
 __device__ __forceinline__ void turn(uint32_t (&turned)[8], uint32_t lo, uint32_t hi) {
@@ -105,7 +145,7 @@ struct GatedBase {
   int lane, cq, rg, nv;
   bool on;
   int64_t c;
-  uint32_t amax = 0;
+  float top = 0.0f;      // max |d|
   float so;
 
   __device__ __forceinline__ GatedBase(const GemmParams& p_, const GatedParams& e_, int64_t first, int lane_)
@@ -116,7 +156,6 @@ struct GatedBase {
     if (!on) rg = 0;
     so = OUT8 ? p.d_scale[0] : 1.0f;
   }
-  __device__ __forceinline__ bool in(int k, int n) const { return FAST ? n > 0 : k < n; }
 
   // Where the strip's row r keeps columns 4 q .. 4 q + 3.
   static __device__ __forceinline__ float4* place(uint8_t* wl, int r, int q) {
@@ -137,13 +176,31 @@ struct GatedBase {
       *place(wl, l16, 4 * j + g) = make_float4(deq(I, j, 0, acc[I][j][0]), deq(I, j, 1, acc[I][j][1]),
                                                deq(I, j, 2, acc[I][j][2]), deq(I, j, 3, acc[I][j][3]));
   }
-  __device__ __forceinline__ void see(const float (&v)[8], int n) {
+  // Takes eight values into the maximum (n: how many of them count) and, as codes of
+  // v * so, into lo and hi.
+  __device__ __forceinline__ void see(const float (&v)[8], int n, uint32_t& lo, uint32_t& hi) {
+    float m;
+    if constexpr (FAST) {
+      m = n > 0 ? max8(v) : 0.0f;
+    } else {
+      float w[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) amax = max_u32(amax, in(k, n) ? abs_bits(v[k]) : 0u);
+      for (int k = 0; k < 8; ++k) w[k] = k < n ? v[k] : 0.0f;
+      m = max8(w);
+    }
+    top = __builtin_elementwise_maximum(top, m);
+    if constexpr (OUT8) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = v[k] * so;
+      const float most = p.d_fp8 == 1 ? Fmt<0>::max : Fmt<1>::max;
+      const bool tame = __builtin_amdgcn_ballot_w64(!(max8(v) * __builtin_fabsf(so) <= most)) == 0;
+      codes_of(p.d_fp8, tame, x, lo, hi);
+    }
   }
   // max |d| of the wavefront as stored.
   __device__ __forceinline__ uint32_t amax_bits() {
-    uint32_t a = wave_max(amax);
+    uint32_t a = wave_max(__float_as_uint(top));
     if (!OUT8 && !p.d_f32) a = (uint32_t)f32_to_bf16_rne(__uint_as_float(a)) << 16;
     return a;
   }
@@ -161,7 +218,7 @@ template <int WTN, bool OUT8, bool FAST>
 struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
   using Base = GatedBase<WTN, WTN / 2, OUT8, FAST>;
   using Base::LPR; using Base::RPL; using Base::p; using Base::e; using Base::lane; using Base::cq; using Base::rg;
-  using Base::nv; using Base::on; using Base::c; using Base::so; using Base::read8; using Base::in;
+  using Base::nv; using Base::on; using Base::c; using Base::so; using Base::read8;
   using Words = uint32_t;            // nothing is read beside the product
   static constexpr int OC = WTN / 2;
   static constexpr bool KEEPS = OC % 32 == 0;   // whole blocks of a checkpoint
@@ -215,15 +272,12 @@ struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
           keep(u, n, a + F, x + nb);
         }
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = g[k];
-      activate<false>(e.act, v, g);
+      act_of(e.act, g, v);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] *= u[k];
-      if (p.d_amax) this->see(v, n);
+      uint32_t lo, hi;
+      this->see(v, n, lo, hi);
       if constexpr (OUT8) {
-        uint32_t lo, hi;
-        codes_of(p.d_fp8, v, so, lo, hi);
         put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
         if (p.D_t) turn(turned, lo, hi);
       } else {
@@ -237,19 +291,23 @@ struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
     asm volatile("" ::: "memory");   // LDS is written and read as different types
   }
 
-  // Eight values of a block's 32 to the checkpoint.
+  // Eight values of a block's 32 to the checkpoint.  Columns past the last output
+  // are zeros (B's rows past its end are read as zeros, their bias is 0), or NaN
+  // where the whole row is, so the block's maximum needs no mask.
   __device__ __forceinline__ void keep(const float (&v)[8], int n, uint8_t* ck, uint8_t* exp) {
-    uint32_t a = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) a = max_u32(a, in(k, n) ? abs_bits(v[k]) : 0u);
+    uint32_t lo, hi, a = __float_as_uint(max8(v));
+    const bool tame = __builtin_amdgcn_ballot_w64(a >= 0x7F800000u) == 0;
     a = max_u32(a, dpp<kXor1>(a));
     a = max_u32(a, dpp<kXor2>(a));
     const uint32_t byte = ck_exponent(a);
-    float x[8];
+    if (__builtin_expect(tame, 1)) {
+      ck_codes(v, byte, lo, hi);
+    } else {
+      float x[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = v[k] * ck_scale(byte);
-    uint32_t lo, hi;
-    encode8<0>(x, lo, hi);
+      for (int k = 0; k < 8; ++k) x[k] = v[k] * ck_scale(byte);
+      encode8<0>(x, lo, hi);
+    }
     put8_codes<LPR, FAST>(ck, n, lo, hi);
     if ((cq & 3) == 0 && n > 0) *exp = (uint8_t)byte;
   }
@@ -279,17 +337,19 @@ struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
   __device__ __forceinline__ void put_dbias(int64_t) {}
 };
 
-// Backward.  KEPT: g and u come from BF16 (0), from a checkpoint (1), or from either (2).
+// Backward: WTN columns are as many outputs of each half.  KEPT: g and u come from BF16
+// (0), from a checkpoint (1), or from either (2).
 template <int WTN, bool OUT8, bool FAST, int KEPT>
 struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
   using Base = GatedBase<WTN, WTN, OUT8, FAST>;
   using Base::LPR; using Base::RPL; using Base::p; using Base::e; using Base::lane; using Base::cq; using Base::rg;
-  using Base::nv; using Base::c; using Base::so; using Base::read8; using Base::in;
+  using Base::nv; using Base::c; using Base::so; using Base::read8;
   static_assert(LPR >= 4, "whole strips");
-  struct Words { v8u g, u; };
+  typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+  using Eight = typename std::conditional<FAST, v4u, v8u>::type;   // (vectors: arrays in arrays go to scratch memory)
+  struct Words { Eight g, u; uint32_t xg, xu; };
   // LDS: the strip, each lane's own words of g and u (32 bytes a row), and (OUT8) the
-  // column-major codes of dg and du of two strips, which leave 32 bytes a column: all
-  // of a wavefront's eight would take more than its part of the stages.
+  // column-major codes of dg and du of two strips, which leave 32 bytes a column.
   static constexpr int FLUSH = 2, TS_ = 16 * FLUSH + 16;
   static constexpr int src_at = 64 * WTN, codes_at = src_at + RPL * 64 * 32;
   static constexpr int bytes(int) { return codes_at + (OUT8 ? 2 * WTN * TS_ : 0); }
@@ -308,14 +368,19 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
     for (int t = 0; t < RPL; ++t) {
       const int64_t m = m0 + rg * RPL + t;
       const int n = m < p.M ? nv : 0;
+      if (n <= 0) {   // zeros, so that no sum or maximum needs a mask
+#pragma unroll
+        for (int k = 0; k < (FAST ? 4 : 5); ++k) o[t].g[k] = o[t].u[k] = 0u;
+        o[t].xg = o[t].xu = 127u;
+      }
       if (coded()) {
         const uint8_t* a = e.ck + m * e.ldck + c;
         const uint8_t* x = e.ck_exp + m * e.ldexp + (c >> 5);
         load_codes(a, n, o[t].g);
         load_codes(a + p.N, n, o[t].u);
         if (n > 0) {
-          o[t].g[2] = x[0];
-          o[t].u[2] = x[ck_blocks(p.N)];
+          o[t].xg = x[0];
+          o[t].xu = x[ck_blocks(p.N)];
         }
       } else {
         const uint16_t* a = reinterpret_cast<const uint16_t*>(e.aux) + m * e.ldaux + c;
@@ -324,7 +389,7 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
       }
     }
   }
-  static __device__ __forceinline__ void load_codes(const uint8_t* a, int n, v8u& w) {
+  static __device__ __forceinline__ void load_codes(const uint8_t* a, int n, Eight& w) {
     if (n <= 0) return;
     if (FAST || n >= 8) {
       struct __attribute__((packed, aligned(FAST ? 4 : 1))) Two { uint32_t a, b; };
@@ -348,7 +413,7 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
     for (int t = 0; t < RPL; ++t) {
       if (coded()) {
         q[t * 64] = make_uint4(o[t].g[0], o[t].g[1], o[t].u[0], o[t].u[1]);
-        reinterpret_cast<uint32_t*>(ol + RPL * 64 * 16)[t * 64 + lane] = o[t].g[2] | (o[t].u[2] << 8);
+        reinterpret_cast<uint32_t*>(ol + RPL * 64 * 16)[t * 64 + lane] = o[t].xg | (o[t].xu << 8);
       } else {
         const uint16_t* a = reinterpret_cast<const uint16_t*>(e.aux) + (m0 + rg * RPL + t) * e.ldaux + c;
         q[t * 64] = words(o[t].g, FAST ? 0u : odd_of(a));
@@ -356,10 +421,11 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
       }
     }
   }
-  static __device__ __forceinline__ uint4 words(const v8u& w, uint32_t s) {
-    if (FAST) return make_uint4(w[0], w[1], w[2], w[3]);
-    return make_uint4(__builtin_amdgcn_alignbyte(w[1], w[0], s), __builtin_amdgcn_alignbyte(w[2], w[1], s),
-                      __builtin_amdgcn_alignbyte(w[3], w[2], s), __builtin_amdgcn_alignbyte(w[4], w[3], s));
+  static __device__ __forceinline__ uint4 words(const Eight& w, uint32_t s) {
+    if constexpr (FAST) return make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      return make_uint4(__builtin_amdgcn_alignbyte(w[1], w[0], s), __builtin_amdgcn_alignbyte(w[2], w[1], s),
+                        __builtin_amdgcn_alignbyte(w[3], w[2], s), __builtin_amdgcn_alignbyte(w[4], w[3], s));
   }
   static __device__ __forceinline__ void widen(const uint4& a, float (&v)[8]) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -398,27 +464,27 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
         g[k] = v[k] * u[k] * s[k];
         u[k] = v[k] * a[k];
       }
+      // (rows past the last and columns past the last have g = u = 0: see fetch)
       if (e.dbias) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          db[0][k] += in(k, n) ? g[k] : 0.0f;
-          db[1][k] += in(k, n) ? u[k] : 0.0f;
+          db[0][k] += g[k];
+          db[1][k] += u[k];
         }
       }
-      if (p.d_amax) {
-        this->see(g, n);
-        this->see(u, n);
-      }
+      uint32_t lo, hi;
+      this->see(g, n, lo, hi);
       if constexpr (OUT8) {
-        uint32_t lo, hi;
-        codes_of(p.d_fp8, g, so, lo, hi);
         put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
         if (p.D_t) turn(tg, lo, hi);
-        codes_of(p.d_fp8, u, so, lo, hi);
+      } else {
+        put8<LPR, FAST>(d, p.d_f32, n, g);
+      }
+      this->see(u, n, lo, hi);
+      if constexpr (OUT8) {
         put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d) + half, n, lo, hi);
         if (p.D_t) turn(tu, lo, hi);
       } else {
-        put8<LPR, FAST>(d, p.d_f32, n, g);
         put8<LPR, FAST>(d + half, p.d_f32, n, u);
       }
       d += p.ldd * esz;
@@ -443,17 +509,16 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
   __device__ __forceinline__ void tile(const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t n0, uint8_t* wl,
                                        Words (&o)[STRIPS][RPL]) {
     static_assert(STRIPS == 1 || STRIPS == TI, "one strip ahead, or all");
+    static_assert(TI == 1 || TI % FLUSH == 0, "whole flushes");
+    constexpr int EACH = TI < FLUSH ? TI : FLUSH;
     this->template each<0, TI>([&](auto itag) {
       constexpr int i = decltype(itag)::value;
       this->template spill<TI, TJ, i>(acc, deq, wl);
       stage(r0 + 16 * i, o[STRIPS == 1 ? 0 : i], wl + src_at);
       if constexpr (STRIPS == 1 && i + 1 < TI) fetch(r0 + 16 * (i + 1), o[0]);
-      rows<TS_>(r0 + 16 * i, wl, wl + src_at, wl + codes_at, 16 * (i % FLUSH));
-      if constexpr (OUT8) {
-        if (p.D_t) {
-          if constexpr (i % FLUSH == FLUSH - 1) flush_t<TS_, 16 * FLUSH>(wl + codes_at, r0 + 16 * (i - FLUSH + 1), n0);
-          else if constexpr (i == TI - 1) flush_t<TS_, 16 * (TI % FLUSH)>(wl + codes_at, r0 + 16 * (TI - TI % FLUSH), n0);
-        }
+      rows<TS_>(r0 + 16 * i, wl, wl + src_at, wl + codes_at, 16 * (i % EACH));
+      if constexpr (OUT8 && i % EACH == EACH - 1) {
+        if (p.D_t) flush_t<TS_, 16 * EACH>(wl + codes_at, r0 + 16 * (i - EACH + 1), n0);
       }
     });
   }
@@ -493,7 +558,9 @@ struct GatedGradOp {
   using Wave = GatedGradWave<WTN, OUT8, false, 2>;
 };
 
-// The epilogue as the large kernels take it (see LinearEp).
+// The epilogue as k_gemm_big takes it (see LinearEp): two wavefronts on a SIMD hide what a
+// strip's way through LDS takes (8192 x 14336 x 4096 with 1x128 scales, backward: 570 us;
+// from the accumulators, as in gemm_gated_direct.h, 630).
 template <typename W, int TI, int TJ, int NW, typename Deq>
 __device__ __forceinline__ void gated_finish(const GemmParams& p, const GatedParams& e, const v4f (&acc)[TI][TJ], Deq&& deq,
                                              int64_t r0, int64_t c0, int64_t part, int lane, int wave, uint8_t* wl) {
@@ -503,8 +570,8 @@ __device__ __forceinline__ void gated_finish(const GemmParams& p, const GatedPar
   w.put_dbias(part);
   if (p.d_amax) ep_amax<NW>(p.d_amax, w.amax_bits(), lane, wave);
 }
-struct GatedEp {
-  static constexpr bool PAIRED = true;
+struct GatedStripEp {
+  static constexpr bool PAIRED = true, DIRECT = false;
   GatedParams e;
   template <bool OUT8, int TI, int TJ, int NW, typename Deq>
   __device__ __forceinline__ void finish(const GemmParams& p, const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t c0,
@@ -513,8 +580,8 @@ struct GatedEp {
   }
 };
 template <int KEPT>
-struct GatedGradEp {
-  static constexpr bool PAIRED = false;
+struct GatedGradStripEp {
+  static constexpr bool PAIRED = false, DIRECT = false;
   GatedParams e;
   template <bool OUT8, int TI, int TJ, int NW, typename Deq>
   __device__ __forceinline__ void finish(const GemmParams& p, const v4f (&acc)[TI][TJ], Deq&& deq, int64_t r0, int64_t c0,

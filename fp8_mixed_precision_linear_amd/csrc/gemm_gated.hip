@@ -82,9 +82,13 @@ bool large_takes(const GemmParams& p, const GatedParams& e) {
   auto dwords = [](const void* q, int64_t ld, int size) {
     return q == nullptr || (((reinterpret_cast<uintptr_t>(q) & 3u) == 0) && ((ld * size) & 3) == 0);
   };
+  // (a wavefront's 128 rows, and 128 of D_t's, stay inside a buffer's 31 bits)
+  auto near = [](const void* q, int64_t ld, int size) { return q == nullptr || ld <= ((int64_t)1 << 23) / size; };
   const bool blocks = p.a_scaling != 0 && p.a_scaling != 5;
-  return p.N % (blocks && !e.backward ? 128 : 8) == 0 && dwords(p.D, p.ldd, p.d_fp8 ? 1 : (p.d_f32 ? 4 : 2)) &&
-         dwords(e.aux, e.ldaux, 2) && dwords(e.ck, e.ldck, 1);
+  const int es = p.d_fp8 ? 1 : (p.d_f32 ? 4 : 2);
+  return p.N % (blocks && !e.backward ? 128 : 32) == 0 && dwords(p.D, p.ldd, es) && dwords(p.D_t, p.ldt, 1) &&
+         dwords(e.aux, e.ldaux, 2) && dwords(e.ck, e.ldck, 1) && near(p.D, p.ldd, es) && near(p.D_t, p.ldt, 1) &&
+         near(e.aux, e.ldaux, 2) && near(e.ck, e.ldck, 1) && near(e.ck_exp, e.ldexp, 1);
 }
 }  // namespace
 

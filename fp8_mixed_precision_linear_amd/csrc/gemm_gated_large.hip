@@ -4,7 +4,7 @@
 namespace fp8lin {
 
 hipError_t launch_gated_large(const GemmParams& p, const GatedParams& e, hipStream_t s) {
-  return p.d_fp8 ? launch_gated_large_as<0, true, GatedEp>(p, e, s) : launch_gated_large_as<0, false, GatedEp>(p, e, s);
+  return p.d_fp8 ? launch_gated_large_as<0, true, GatedEp, GatedStripEp>(p, e, s) : launch_gated_large_as<0, false, GatedEp, GatedStripEp>(p, e, s);
 }
 
 }  // namespace fp8lin

@@ -47,6 +47,23 @@ enum : int { W4_TENSOR = 0, W4_ROWS = 1, W4_MX = 2 };
 // fit in the wavefront's 32 KB)
 constexpr int W4_OUT8_PASSES = 2;
 
+// Which row of A, and which row of B (PAIRED: which pair's), of the tile's stands in row v
+// of a stage.  An MFMA leaves lane (g, l16) with row l16 of a row-tile i and rows 4 g + q of
+// a column-tile j; placed DIRECT, a lane has rows 64 h + 4 l16 + t (i = 4 h + t) of its
+// wavefront's 128 and two runs r of 16 columns, 64 r + 16 g + 4 (j mod 4) + q, j = 4 r ..
+// (PAIRED: one run of pairs, 16 g + 4 (j / 2) + q), the four lanes of a row side by side.
+template <bool DIRECT, bool PAIRED>
+struct TilePlace {
+  static __device__ __forceinline__ int a_row(int v) {
+    return DIRECT ? (v & ~63) + 4 * (v & 15) + ((v >> 4) & 3) : v;
+  }
+  static __device__ __forceinline__ int b_row(int v) {
+    if (!DIRECT) return PAIRED ? pair_of(v) : v;
+    const int w = v >> 7, j = (v >> 4) & 7, g = (v >> 2) & 3, q = v & 3;
+    return PAIRED ? 64 * w + 16 * g + 4 * (j >> 1) + q : 128 * w + 64 * (j >> 2) + 16 * g + 4 * (j & 3) + q;
+  }
+};
+
 // KT: K is not a multiple of the step (chunks past K map to the
 // out-of-range marker, step by step); OUT8: FP8 output quantised in the
 // epilogue (codes, optional transposed copy, amax of the unquantised
@@ -60,15 +77,18 @@ constexpr int W4_OUT8_PASSES = 2;
 // a per-tensor operand's scale goes to the epilogue).
 // EP: the linear's epilogue (gemm_ep.h) in place of the plain one, its arguments
 // in `ep` (NoEpilogue: none).  A PAIRED one's columns are pairs of B's rows (see
-// k_gemm_big; N a multiple of 128 in the block modes, of 1 in the others).
+// k_gemm_big; N a multiple of 128 in the block modes).  A DIRECT one takes the
+// accumulators as they are, rows and columns placed for it (TilePlace), and its first
+// reads are on their way before the last step.
 template <int AF, int BF, bool KT, bool OUT8, int MODE, typename EP = NoEpilogue>
 __global__ void __launch_bounds__(W4_THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
 k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   constexpr bool ROWS = MODE == W4_ROWS, MX = MODE >= W4_MX;
   constexpr bool SA_ROWS = MX && ((MODE - W4_MX) & 1), SB_COL = MX && ((MODE - W4_MX) & 2);
-  constexpr bool PAIRED = EP::PAIRED;
+  constexpr bool PAIRED = EP::PAIRED, DIRECT = EP::DIRECT;
+  using Place = TilePlace<DIRECT, PAIRED>;
   static_assert(!(MX && KT), "block scales make K a multiple of the step");
-  static_assert(!(PAIRED && SB_COL), "pairs: blocks of B");
+  static_assert(!((PAIRED || DIRECT) && SB_COL), "pairs and placed tiles: blocks of B");
   // a stage: A, B, then (block modes) 256 row scales of A and of B
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][MX ? STAGE : W4_STAGE];
   // per-row scales of the tile's 256 D rows and 256 D columns (rows clamped
@@ -128,8 +148,8 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
 #pragma unroll
   for (int it = 0; it < 8; ++it) {
     const int row = 64 * wave + 8 * it + (lane >> 3);
-    ro[0][it] = (uint32_t)(row * lda);
-    ro[1][it] = (uint32_t)((PAIRED ? pair_of(row) : row) * ldb);
+    ro[0][it] = (uint32_t)(Place::a_row(row) * lda);
+    ro[1][it] = (uint32_t)(Place::b_row(row) * ldb);
   }
 #pragma unroll
   for (int par = 0; par < 2; ++par)
@@ -179,7 +199,7 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   if constexpr (ROWS) {   // thread t: A's scale of D row m0 + t, then B's of column n0 + t
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t r = (h == 0 ? m0 : n0) + (PAIRED && h ? pair_of(tid) : tid), lim = h == 0 ? M : N;
+      const int64_t r = h == 0 ? m0 + Place::a_row(tid) : n0 + Place::b_row(tid), lim = h == 0 ? M : N;
       const bool row_mode = (h == 0 ? p.a_scaling : p.b_scaling) == 5;
       const int64_t row = (r < lim ? r : lim - 1) + (PAIRED && h && half_of(tid) ? N : 0);
       rs_tab[h * BM + tid] = (h == 0 ? p.a_sinv : p.b_sinv)[row_mode ? row : 0];
@@ -219,7 +239,7 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   // their E8M0 codes are taken at the MFMA, long after the read returned
   float ea[8], eb[8];
   auto ea_of = [&](const uint8_t* S, int i) {
-    return reinterpret_cast<const float*>(S + SA_OFF)[wm * 128 + 16 * i + l16];
+    return reinterpret_cast<const float*>(S + SA_OFF)[wm * 128 + Place::a_row(16 * i + l16)];
   };
   auto eb_of = [&](const uint8_t* S, int j) {
     return reinterpret_cast<const float*>(S + SB_OFF)[wn * 128 + 16 * j + l16];
@@ -313,6 +333,12 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
     step(F, T, lds[kb & 1], lds[(kb + 1) & 1], kb);
     ++kb;
   }
+  auto run = [&] {
+    if constexpr (DIRECT)
+      return typename EP::template Run<OUT8, 8, 8, 4>(p, ep.e, m0 + wm * 128, (int64_t)tn * BN + wn * 128, lane);
+    else return 0;
+  }();
+  if constexpr (DIRECT) run.ahead();
   step(F, F, lds[kb & 1], lds[kb & 1], kb);
 
   // ---- epilogue (k_gemm_big's, for 128 x 128 wavefront tiles and 32 KB of
@@ -330,7 +356,10 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
     else
       return (x * sa) * sb;
   };
-  if constexpr (!std::is_same_v<EP, NoEpilogue>) {
+  if constexpr (DIRECT) {
+    run.finish(acc, deq, tm * 2 + wm, lane, wave);
+    return;
+  } else if constexpr (!std::is_same_v<EP, NoEpilogue>) {
     __syncthreads();   // every wavefront is done reading both stages
     ep.template finish<OUT8, 8, 8, 4>(p, acc, deq, m0 + wm * 128, (int64_t)tn * BN + wn * 128, tm * 2 + wm, lane, wave,
                                       &lds[0][0] + wave * 32768);
