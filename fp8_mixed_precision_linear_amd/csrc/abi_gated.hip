@@ -82,8 +82,8 @@ fp8_status fp8_gated_linear_plan(const fp8_gemm_args* gemm, const fp8_gated_args
   if (st != FP8_OK) return st;
   if (plan == nullptr) return FP8_ERR_NULL;
   const EpPlan t = gated_plan(p, e);
-  plan->kernel = t.large ? FP8_EP_LARGE : (t.skinny ? FP8_EP_FEW_ROWS : FP8_EP_TILES);
-  plan->tile_rows = t.large ? 256 : (t.skinny ? 16 : t.bm);
+  plan->kernel = t.large || t.mid ? FP8_EP_LARGE : (t.skinny ? FP8_EP_FEW_ROWS : FP8_EP_TILES);
+  plan->tile_rows = t.large ? 256 : t.mid ? 160 : (t.skinny ? 16 : t.bm);
   plan->k_parts = t.splits;
   return FP8_OK;
 }

@@ -79,12 +79,13 @@ struct TileCost {
 };
 constexpr TileCost kCost[2][4] = {{{32, 0.35f, 0.0f}, {64, 0.44f, 0.64f}, {128, 0.74f, 0.95f}, {256, 1.45f, 0.0f}},
                                   {{32, 0.50f, 0.0f}, {64, 0.66f, 0.92f}, {128, 1.15f, 1.50f}, {256, 1.75f, 0.0f}}};
+constexpr TileCost kMidCost = {160, 1.2f, 0.0f};   // (gemm_gated_mid.hip)
 
 // What a product takes on tiles of c.bm rows with K in `splits` parts: a launch
 // and an epilogue, rounds of as many workgroups as run at once, and for parts a
 // second launch and the sums' way through memory.
 float tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int splits, int64_t cu) {
-  const int64_t bn = c.bm == 256 ? 256 : 128;
+  const int64_t bn = c.bm > 128 ? 256 : 128;
   const int64_t wgs = (M + c.bm - 1) / c.bm * ((N + bn - 1) / bn) * splits;
   const int64_t at_once = c.two > 0.0f ? 2 * cu : cu, full = wgs / at_once, rest = wgs - full * at_once;
   const float round = c.two > 0.0f ? c.two : c.alone;
@@ -123,7 +124,9 @@ EpPlan ep_plan(const GemmParams& p) {
         plan.bm = cost[i].bm;
         plan.splits = splits;
       }
-    plan.large = layer && p.K > 0 && tile_time(cost[3], p.M, p.N, nk, 1, cu) < best;
+    const float large = tile_time(cost[3], p.M, p.N, nk, 1, cu);
+    plan.large = layer && p.K > 0 && large < best;
+    plan.mid = layer && p.K > 0 && tile_time(kMidCost, p.M, p.N, nk, 1, cu) < (large < best ? large : best);
   }
   // Rows of column sums: the wavefronts' of the tiles, of the join or of the
   // few-row kernel; room for the tiles' too where a product of the large kernels'

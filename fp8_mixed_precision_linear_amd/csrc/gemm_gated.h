@@ -116,7 +116,7 @@ __device__ __forceinline__ void put_columns(uint8_t* d_t, int64_t ldt, const uin
   constexpr int LPC = ROWS / 16;
   const int q = lane % LPC;
   left -= 16 * q;
-  if (left <= 0) return;
+  if (left <= 0 || lane >= 64 / LPC * LPC) return;
   uint8_t* dst = d_t + n * ldt + m + 16 * q;
 #pragma unroll 2
   for (int k = lane / LPC; k < cols; k += 64 / LPC) {

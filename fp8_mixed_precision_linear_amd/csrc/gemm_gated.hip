@@ -77,6 +77,7 @@ EpPlan plan_of(const GemmParams& p, int backward, bool tiles) {
 EpPlan gated_plan(const GemmParams& p, int backward) { return plan_of(p, backward, !backward); }
 
 namespace {
+bool blocks(const GemmParams& p) { return p.a_scaling != 0 && p.a_scaling != 5; }
 // What the large kernels take: see gemm_gated_large.h.
 bool large_takes(const GemmParams& p, const GatedParams& e) {
   auto dwords = [](const void* q, int64_t ld, int size) {
@@ -84,9 +85,8 @@ bool large_takes(const GemmParams& p, const GatedParams& e) {
   };
   // (a wavefront's 128 rows, and 128 of D_t's, stay inside a buffer's 31 bits)
   auto near = [](const void* q, int64_t ld, int size) { return q == nullptr || ld <= ((int64_t)1 << 23) / size; };
-  const bool blocks = p.a_scaling != 0 && p.a_scaling != 5;
   const int es = p.d_fp8 ? 1 : (p.d_f32 ? 4 : 2);
-  return p.N % (blocks && !e.backward ? 128 : 32) == 0 && dwords(p.D, p.ldd, es) && dwords(p.D_t, p.ldt, 1) &&
+  return p.N % (blocks(p) && !e.backward ? 128 : 32) == 0 && dwords(p.D, p.ldd, es) && dwords(p.D_t, p.ldt, 1) &&
          dwords(e.aux, e.ldaux, 2) && dwords(e.ck, e.ldck, 1) && near(p.D, p.ldd, es) && near(p.D_t, p.ldt, 1) &&
          near(e.aux, e.ldaux, 2) && near(e.ck, e.ldck, 1) && near(e.ck_exp, e.ldexp, 1);
 }
@@ -94,8 +94,10 @@ bool large_takes(const GemmParams& p, const GatedParams& e) {
 
 EpPlan gated_plan(const GemmParams& p, const GatedParams& e) {
   EpPlan plan = plan_of(p, e.backward, !e.backward && e.ck != nullptr);
-  plan.large = plan.large && large_takes(p, e);
-  if (plan.large) plan.splits = 1;
+  const bool takes = large_takes(p, e);
+  plan.mid = plan.mid && takes && !e.backward && !blocks(p);
+  plan.large = plan.large && takes && !plan.mid;
+  if (plan.large || plan.mid) plan.splits = 1;
   return plan;
 }
 
@@ -113,6 +115,7 @@ hipError_t launch_gated(const GemmParams& p0, GatedParams e, uint8_t* ws, hipStr
   e.splits = plan.splits;
   // (powers of two on every block-scaled operand go into the matrix instruction; beside
   // others, and for few rows, they are binary32 scales of the same layouts)
+  if (plan.mid) return launch_gated_mid(p, e, s);
   if (plan.large) {
     const hipError_t err = !e.backward ? launch_gated_large(p, e, s)
                            : p.a_fmt == 0 ? launch_gated_grad_large(p, e, s) : launch_gated_grad_large_e5m2(p, e, s);

@@ -80,7 +80,10 @@ struct TilePlace {
 // k_gemm_big; N a multiple of 128 in the block modes).  A DIRECT one takes the
 // accumulators as they are, rows and columns placed for it (TilePlace), and its first
 // reads are on their way before the last step.
-template <int AF, int BF, bool KT, bool OUT8, int MODE, typename EP = NoEpilogue>
+// TI: 16-row tiles of a wavefront, 8 unless the epilogue takes fewer (32 TI rows a
+// workgroup; the step's first TI / 2 row-tiles go row by row, the rest column by column;
+// 160 rows have three stages).
+template <int AF, int BF, bool KT, bool OUT8, int MODE, typename EP = NoEpilogue, int TI = 8>
 __global__ void __launch_bounds__(W4_THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
 k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   constexpr bool ROWS = MODE == W4_ROWS, MX = MODE >= W4_MX;
@@ -89,8 +92,13 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   using Place = TilePlace<DIRECT, PAIRED>;
   static_assert(!(MX && KT), "block scales make K a multiple of the step");
   static_assert(!((PAIRED || DIRECT) && SB_COL), "pairs and placed tiles: blocks of B");
+  constexpr int BMT = 32 * TI, R1 = TI / 2, R2 = TI - R1, NQ = TI + 8;   // rows, row-tiles of each part, DMA per stage
+  static_assert(TI == 8 || (TI >= 5 && TI < 8 && !DIRECT && !std::is_same_v<EP, NoEpilogue> && !MX),
+                "fewer rows: strips, no block scales");
+  constexpr int AB = BMT * BK;   // B's place in a stage
+  constexpr int NS = TI == 5 ? 3 : 2;   // stages: 160 rows leave room for a third
   // a stage: A, B, then (block modes) 256 row scales of A and of B
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][MX ? STAGE : W4_STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NS][MX ? STAGE : AB + B_BYTES];
   // per-row scales of the tile's 256 D rows and 256 D columns (rows clamped
   // into D for edge tiles), read in the epilogue
   __shared__ float rs_tab[ROWS ? BM + BN : 1];
@@ -115,9 +123,9 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   const int in_group = bid - group * GROUP_M * tiles_n;
   const int tm = first_m + in_group % gm, tn = in_group / gm;
   constexpr int BNP = PAIRED ? BN / 2 : BN;
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BNP;
+  const int64_t m0 = (int64_t)tm * BMT, n0 = (int64_t)tn * BNP;
 
-  const int64_t rows_a = min((int64_t)BM, M - m0), rows_b = min((int64_t)BNP, N - n0);
+  const int64_t rows_a = min((int64_t)BMT, M - m0), rows_b = min((int64_t)BNP, N - n0);
   const i32x4 ra = make_rsrc(p.A + m0 * p.lda, (uint32_t)(rows_a * p.lda));
   const i32x4 rb = make_rsrc(p.B + n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
   const i32x4 rb2 = PAIRED ? make_rsrc(p.B + (N + n0) * p.ldb, (uint32_t)(rows_b * p.ldb)) : rb;
@@ -136,7 +144,7 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   float so = 1.0f;
   if constexpr (OUT8) so = p.d_scale[0];
 
-  // ---- DMA: wavefront w fills rows 64w .. 64w + 63 of A and of B, 8 rows
+  // ---- DMA: wavefront w fills 64 rows of B and 8 TI rows of A, 8 rows
   // per instruction; lane l lands in row 8 it + l / 8 of the group, stored
   // chunk l % 8, and fetches the K chunk the swizzle puts there, which
   // depends only on the parity of it.  The row offset stays in the lane
@@ -144,24 +152,26 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   // and read zeros; with K a multiple of the step the step's K offset rides
   // in the scalar offset, otherwise chunks past K get the out-of-range
   // marker.
-  uint32_t ro[2][8], kcl[2];
+  uint32_t ro[2][8], kcl[2], kca[2];
 #pragma unroll
   for (int it = 0; it < 8; ++it) {
-    const int row = 64 * wave + 8 * it + (lane >> 3);
-    ro[0][it] = (uint32_t)(Place::a_row(row) * lda);
-    ro[1][it] = (uint32_t)(Place::b_row(row) * ldb);
+    if (it < TI) ro[0][it] = (uint32_t)(Place::a_row(8 * TI * wave + 8 * it + (lane >> 3)) * lda);
+    ro[1][it] = (uint32_t)(Place::b_row(64 * wave + 8 * it + (lane >> 3)) * ldb);
   }
 #pragma unroll
-  for (int par = 0; par < 2; ++par)
+  for (int par = 0; par < 2; ++par) {
     kcl[par] = (uint32_t)(16 * ((lane & 7) ^ swz(64 * wave + 8 * par + (lane >> 3))));
-  auto load = [&](int kb, const uint8_t* base, int q) {   // q: 0..7 A, 8..15 B
-    const int o = q >> 3, it = q & 7;
-    const uint32_t dst = lds_addr(base) + (o ? A_BYTES : 0) + (64 * wave + 8 * it) * BK;
+    kca[par] = TI % 2 == 0 ? kcl[par] : (uint32_t)(16 * ((lane & 7) ^ swz(8 * TI * wave + 8 * par + (lane >> 3))));
+  }
+  auto load = [&](int kb, const uint8_t* base, int q) {   // q: 0 .. TI - 1 A, then 8 of B
+    const int o = q >= TI ? 1 : 0, it = o ? q - TI : q;
+    const uint32_t dst = lds_addr(base) + (o ? AB + 64 * wave * BK : 8 * TI * wave * BK) + 8 * it * BK;
     const i32x4& rs = o ? (PAIRED && half_of(8 * it) ? rb2 : rb) : ra;
+    const uint32_t kl = o ? kcl[it & 1] : kca[it & 1];
     if constexpr (!KT) {
-      dma16s(dst, ro[o][it] + kcl[it & 1], rs, (uint32_t)(kb * BK));
+      dma16s(dst, ro[o][it] + kl, rs, (uint32_t)(kb * BK));
     } else {
-      const int kc = kb * BK + (int)kcl[it & 1];
+      const int kc = kb * BK + (int)kl;
       dma16(dst, kc < (int)K ? ro[o][it] + (uint32_t)kc : kOOB, rs);
     }
   };
@@ -180,21 +190,24 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
     }
   };
 
-  v4f acc[8][8];
+  v4f acc[TI][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  // the first two stages go out together; wait for the first (16 DMA
+  // the first two stages go out together; wait for the first (NQ DMA
   // instructions per stage and wavefront, counted down in issue order)
 #pragma unroll
-  for (int q = 0; q < 16; ++q) load(0, lds[0], q);
+  for (int q = 0; q < NQ; ++q) load(0, lds[0], q);
   load_scales(0, lds[0]);
-  if (nk > 1) {
 #pragma unroll
-    for (int q = 0; q < 16; ++q) load(1, lds[1], q);
-    load_scales(1, lds[1]);
+  for (int n = 1; n < NS; ++n) {
+    if (nk > n) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) load(n, lds[n], q);
+      load_scales(n, lds[n]);
+    }
   }
   if constexpr (ROWS) {   // thread t: A's scale of D row m0 + t, then B's of column n0 + t
 #pragma unroll
@@ -223,30 +236,31 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   }
   // stage 0 done (in the block modes up to 2 more DMA instructions per
   // stage: the wait then covers part of stage 1 as well)
-  if (nk > 1) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+  if (NS > 2 && nk > 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * NQ) : "memory");
+  else if (nk > 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NQ) : "memory");
   else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
 
   // Lane (g, l16) of the transposed MFMA (B is its first operand) holds D
   // row 16 i + l16, columns 16 j + 4 g .. +3 of the wavefront's tile.
-  const int ar = wm * 128 + l16, br = wn * 128 + l16;
-  v8i b[8], a[2], h[4];
+  const int ar = wm * 16 * TI + l16, br = wn * 128 + l16;
+  v8i b[8], a[2], h[R2];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = frag(lds[0] + A_BYTES, br + 16 * j, g);
+  for (int j = 0; j < 8; ++j) b[j] = frag(lds[0] + AB, br + 16 * j, g);
   a[0] = frag(lds[0], ar, g);
   // block modes: the step's scales of A's row-tiles (lane l16: row
   // 16 i + l16) and of B's column-tiles (column 16 j + l16), kept as read;
   // their E8M0 codes are taken at the MFMA, long after the read returned
-  float ea[8], eb[8];
+  float ea[TI], eb[8];
   auto ea_of = [&](const uint8_t* S, int i) {
-    return reinterpret_cast<const float*>(S + SA_OFF)[wm * 128 + Place::a_row(16 * i + l16)];
+    return reinterpret_cast<const float*>(S + SA_OFF)[wm * 16 * TI + Place::a_row(16 * i + l16)];
   };
   auto eb_of = [&](const uint8_t* S, int j) {
     return reinterpret_cast<const float*>(S + SB_OFF)[wn * 128 + 16 * j + l16];
   };
   if constexpr (SA_ROWS) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ea[i] = ea_of(lds[0], i);
+    for (int i = 0; i < TI; ++i) ea[i] = ea_of(lds[0], i);
   }
   if constexpr (SB_COL) {
 #pragma unroll
@@ -264,20 +278,22 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   // One K step on stage X, with B's fragments and row-tile 0's A fragment
   // in registers; Y is the next step's stage.  The scheduling barriers keep
   // the compiler to this order.
-  auto step = [&](auto dmatag, auto nexttag, const uint8_t* X, const uint8_t* Y, int kb) {
+  auto step = [&](auto dmatag, auto nexttag, auto lefttag, const uint8_t* X, const uint8_t* Y, int kb) {
     constexpr bool DMA = decltype(dmatag)::value;    // issue the DMA of step kb + 2
     constexpr bool NEXT = decltype(nexttag)::value;  // read step kb + 1's fragments
+    constexpr int LEFT = decltype(lefttag)::value ? (NS - 2) * NQ : 0;   // DMA instructions of step kb + 2 in flight
     uint32_t eu = 0;
     if constexpr (MX && !(SA_ROWS && SB_COL)) eu = __float_as_uint(su_tab[wave][kb]);
     __builtin_amdgcn_sched_barrier(0);
-    // row-tiles 0..3, row by row: the next row-tile's A fragment is read
+    // row-tiles 0..3 (R1 of them), row by row: the next row-tile's A fragment is read
     // after this row's first MFMA, row-tile i + 4's after its fifth
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R1; ++i) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (j == 1 && i < 3) a[(i + 1) & 1] = frag(X, ar + 16 * (i + 1), g);
-        if (j == 5) h[i] = frag(X, ar + 16 * (i + 4), g);
+        if (j == 1 && i < R1 - 1) a[(i + 1) & 1] = frag(X, ar + 16 * (i + 1), g);
+        if (j == 5) h[i] = frag(X, ar + 16 * (i + R1), g);
+        if (R2 > R1 && j == 5 && i == R1 - 1) h[R1] = frag(X, ar + 16 * (R1 + R1), g);
         if (j == 1 || j == 5) __builtin_amdgcn_sched_barrier(0);
         acc[i][j] = mm(b[j], a[i & 1], acc[i][j], i, j, eu);
         if (j == 0 || j == 4) __builtin_amdgcn_sched_barrier(0);
@@ -287,13 +303,13 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
     if constexpr (NEXT) {
       // every read of X is issued: once they and this wavefront's DMA of Y
       // are done everywhere, Y may be read and X refilled
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT) : "memory");
       __syncthreads();
       __builtin_amdgcn_sched_barrier(0);
       a[0] = frag(Y, ar, g);
       if constexpr (SA_ROWS) {   // row-tiles 0..3 are done with theirs
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ea[i] = ea_of(Y, i);
+        for (int i = 0; i < R1; ++i) ea[i] = ea_of(Y, i);
       }
     }
     // row-tiles 4..7, column by column: two DMA instructions of step kb + 2
@@ -302,35 +318,40 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
 #pragma unroll
-      for (int i = 4; i < 8; ++i) {
-        acc[i][j] = mm(b[j], h[i - 4], acc[i][j], i, j, eu);
+      for (int i = R1; i < TI; ++i) {
+        acc[i][j] = mm(b[j], h[i - R1], acc[i][j], i, j, eu);
         if constexpr (DMA) {
-          if (i == 4 || i == 6) {
+          if ((i == R1 || i == R1 + 2) && 2 * j + (i - R1) / 2 < NQ) {
             __builtin_amdgcn_sched_barrier(0);
-            load(kb + 2, X, 2 * j + (i - 4) / 2);
+            load(kb + NS, X, 2 * j + (i - R1) / 2);
             __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
-      if constexpr (NEXT) b[j] = frag(Y + A_BYTES, br + 16 * j, g);
+      if constexpr (NEXT) b[j] = frag(Y + AB, br + 16 * j, g);
       if constexpr (SB_COL && NEXT) eb[j] = eb_of(Y, j);
       if constexpr (DMA) {
-        if (j == 7) load_scales(kb + 2, X);
+        if (j == 7) load_scales(kb + NS, X);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (SA_ROWS && NEXT) {
 #pragma unroll
-      for (int i = 4; i < 8; ++i) ea[i] = ea_of(Y, i);
+      for (int i = R1; i < TI; ++i) ea[i] = ea_of(Y, i);
     }
   };
 
   const std::true_type T{};
   const std::false_type F{};
   int kb = 0;
-  for (; kb + 2 < nk; ++kb) step(T, T, lds[kb & 1], lds[(kb + 1) & 1], kb);
+  auto stage = [&](int k) -> const uint8_t* { return lds[NS == 2 ? k & 1 : k % NS]; };
+  for (; kb + NS < nk; ++kb) step(T, T, T, stage(kb), stage(kb + 1), kb);
+  if (NS > 2 && kb + 2 < nk) {
+    step(F, T, T, stage(kb), stage(kb + 1), kb);
+    ++kb;
+  }
   if (kb + 1 < nk) {
-    step(F, T, lds[kb & 1], lds[(kb + 1) & 1], kb);
+    step(F, T, F, stage(kb), stage(kb + 1), kb);
     ++kb;
   }
   auto run = [&] {
@@ -339,7 +360,7 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
     else return 0;
   }();
   if constexpr (DIRECT) run.ahead();
-  step(F, F, lds[kb & 1], lds[kb & 1], kb);
+  step(F, F, F, stage(kb), stage(kb), kb);
 
   // ---- epilogue (k_gemm_big's, for 128 x 128 wavefront tiles and 32 KB of
   // staging per wavefront).  With per-tensor scales every nonzero
@@ -352,37 +373,36 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   const bool may_sub = MODE != W4_TENSOR || !(lo >= 1.17549435e-38f);   // NaN scales: check
   auto deq = [&](int i, int j, int q, float x) -> float {
     if constexpr (ROWS)
-      return (x * rs_tab[wm * 128 + 16 * i + l16]) * rs_tab[BM + wn * 128 + 16 * j + 4 * g + q];
+      return (x * rs_tab[wm * 16 * TI + 16 * i + l16]) * rs_tab[BM + wn * 128 + 16 * j + 4 * g + q];
     else
       return (x * sa) * sb;
   };
   if constexpr (DIRECT) {
     run.finish(acc, deq, tm * 2 + wm, lane, wave);
-    return;
   } else if constexpr (!std::is_same_v<EP, NoEpilogue>) {
     __syncthreads();   // every wavefront is done reading both stages
-    ep.template finish<OUT8, 8, 8, 4>(p, acc, deq, m0 + wm * 128, (int64_t)tn * BN + wn * 128, tm * 2 + wm, lane, wave,
+    ep.template finish<OUT8, TI, 8, 4>(p, acc, deq, m0 + wm * 16 * TI, (int64_t)tn * BN + wn * 128, tm * 2 + wm, lane, wave,
                                       &lds[0][0] + wave * 32768);
-    return;
-  }
-  const int esz = OUT8 ? 1 : (p.d_f32 ? 4 : 2);
-  const bool staged = (m0 + BM <= M) && (n0 + BN <= N) && ((p.ldd * esz) % 16 == 0) &&
-                      ((reinterpret_cast<uintptr_t>(p.D) & 15u) == 0) &&
-                      (!OUT8 || p.D_t == nullptr ||
-                       ((p.ldt % 16 == 0) && ((reinterpret_cast<uintptr_t>(p.D_t) & 15u) == 0)));
-  uint32_t amax_bits;
-  if (staged) {
-    __syncthreads();   // every wavefront is done reading both stages
-    uint8_t* wl = &lds[0][0] + wave * 32768;
-    if constexpr (OUT8)
-      amax_bits = store_staged8<8, 8, W4_OUT8_PASSES>(p, acc, deq, so, m0 + wm * 128, n0 + wn * 128, lane, wl);
-    else
-      amax_bits = store_staged<8, 8, 32768>(p, acc, deq, may_sub, m0 + wm * 128, n0 + wn * 128,
-                                            lane, wl);
   } else {
-    amax_bits = store_edge<8, 8, OUT8>(p, acc, deq, so, m0 + wm * 128, n0 + wn * 128, lane);
+    const int esz = OUT8 ? 1 : (p.d_f32 ? 4 : 2);
+    const bool staged = (m0 + BM <= M) && (n0 + BN <= N) && ((p.ldd * esz) % 16 == 0) &&
+                        ((reinterpret_cast<uintptr_t>(p.D) & 15u) == 0) &&
+                        (!OUT8 || p.D_t == nullptr ||
+                         ((p.ldt % 16 == 0) && ((reinterpret_cast<uintptr_t>(p.D_t) & 15u) == 0)));
+    uint32_t amax_bits;
+    if (staged) {
+      __syncthreads();   // every wavefront is done reading both stages
+      uint8_t* wl = &lds[0][0] + wave * 32768;
+      if constexpr (OUT8)
+        amax_bits = store_staged8<8, 8, W4_OUT8_PASSES>(p, acc, deq, so, m0 + wm * 128, n0 + wn * 128, lane, wl);
+      else
+        amax_bits = store_staged<8, 8, 32768>(p, acc, deq, may_sub, m0 + wm * 128, n0 + wn * 128,
+                                              lane, wl);
+    } else {
+      amax_bits = store_edge<8, 8, OUT8>(p, acc, deq, so, m0 + wm * 128, n0 + wn * 128, lane);
+    }
+    if (p.d_amax) workgroup_amax<4>(p.d_amax, amax_bits, lane, wave);
   }
-  if (p.d_amax) workgroup_amax<4>(p.d_amax, amax_bits, lane, wave);
 }
 
 template <int AF, int BF, bool OUT8, int MODE>

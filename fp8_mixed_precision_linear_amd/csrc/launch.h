@@ -199,6 +199,7 @@ struct EpParams {
 struct EpPlan {
   int bm, bn, splits;
   bool large;   // 256 x 256 tiles of the large kernels
+  bool mid;     // 160 x 256 tiles would be faster (the gated pair has them)
   bool skinny;  // few rows: weights streamed to registers
   int64_t parts, large_parts;   // rows of column sums; on the large kernels
   int64_t ldw, part_bytes, sums_bytes;
@@ -245,6 +246,7 @@ hipError_t launch_gated_grad_tile(const GemmParams& p, const GatedParams& e, con
 hipError_t launch_gated_grad_tile_blk(const GemmParams& p, const GatedParams& e, const EpPlan& plan, hipStream_t s);
 // (power-of-two scalings keep their codes, as in launch_gemm_ep_large)
 hipError_t launch_gated_large(const GemmParams& p, const GatedParams& e, hipStream_t s);
+hipError_t launch_gated_mid(const GemmParams& p, const GatedParams& e, hipStream_t s);
 hipError_t launch_gated_grad_large(const GemmParams& p, const GatedParams& e, hipStream_t s);
 hipError_t launch_gated_grad_large_e5m2(const GemmParams& p, const GatedParams& e, hipStream_t s);
 hipError_t launch_gated_skinny(const GemmParams& p, const GatedParams& e, hipStream_t s);

@@ -643,7 +643,7 @@ fp8_status fp8_scaled_gemm_ep(const fp8_gemm_args* gemm, const fp8_epilogue_args
 typedef enum {
   FP8_EP_FEW_ROWS = 0,   /* up to 16 rows, weights streamed from memory */
   FP8_EP_TILES = 1,      /* tiles of tile_rows x 128, K in k_parts parts */
-  FP8_EP_LARGE = 2       /* tiles of 256 x 256 */
+  FP8_EP_LARGE = 2       /* tiles of tile_rows x 256 (256, of the gated pair also 160) */
 } fp8_ep_kernel;
 typedef struct {
   fp8_ep_kernel kernel;
