@@ -539,7 +539,7 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
       for (int k = 0; k < 8; ++k)
 #pragma unroll
         for (int off = LPR; off < 64; off <<= 1) db[h][k] += __shfl_xor(db[h][k], off, 64);
-      if (rg == 0 && nv > 0) store8(e.part, 1, (2 * row + h) * p.N + c, nv, db[h]);
+      if (rg == 0 && nv > 0) store8(e.part, e.part_f32, (2 * row + h) * p.N + c, nv, db[h]);
     }
   }
 };

@@ -109,7 +109,10 @@ hipError_t launch_gated(const GemmParams& p0, GatedParams e, uint8_t* ws, hipStr
   }
   if (p.N == 0) return hipSuccess;
   const EpPlan plan = gated_plan(p, e);
-  e.part = reinterpret_cast<float*>(ws);
+  // (the only row of column sums is the bias gradient: up to 32 rows, 3 us less)
+  const bool joined = e.dbias != nullptr && (plan.large || plan.parts != 1);
+  e.part = e.dbias && !joined ? static_cast<float*>(e.dbias) : reinterpret_cast<float*>(ws);
+  e.part_f32 = joined || e.bias_f32;
   e.sums = reinterpret_cast<float*>(ws + plan.part_bytes);
   e.ldw = plan.ldw;
   e.splits = plan.splits;
@@ -120,7 +123,7 @@ hipError_t launch_gated(const GemmParams& p0, GatedParams e, uint8_t* ws, hipStr
     const hipError_t err = !e.backward ? launch_gated_large(p, e, s)
                            : p.a_fmt == 0 ? launch_gated_grad_large(p, e, s) : launch_gated_grad_large_e5m2(p, e, s);
     if (err != hipSuccess) return err;
-    return e.dbias ? launch_ep_dbias(e.part, plan.large_parts, 2 * p.N, e.dbias, e.bias_f32, s) : hipSuccess;
+    return joined ? launch_ep_dbias(e.part, plan.large_parts, 2 * p.N, e.dbias, e.bias_f32, s) : hipSuccess;
   }
   const bool promoted = p.a_scaling == 1 || p.a_scaling == 2 || p.b_scaling == 1 || p.b_scaling == 2;
   if (p.a_scaling == 3 || p.a_scaling == 4) p.a_scaling -= 2;
@@ -136,7 +139,7 @@ hipError_t launch_gated(const GemmParams& p0, GatedParams e, uint8_t* ws, hipStr
       if (err != hipSuccess) return err;
     }
   }
-  return e.dbias ? launch_ep_dbias(e.part, plan.parts, 2 * p.N, e.dbias, e.bias_f32, s) : hipSuccess;
+  return joined ? launch_ep_dbias(e.part, plan.parts, 2 * p.N, e.dbias, e.bias_f32, s) : hipSuccess;
 }
 
 }  // namespace fp8lin

@@ -232,9 +232,10 @@ struct GatedParams {
   uint8_t* ck_exp;    // [M][2 ceil(F / 32)]
   int64_t ldexp;
   void* dbias;        // backward: [2 F]
-  float* part;        // workspace: column sums
+  float* part;        // workspace: column sums (one row of them: dbias itself, in its type)
   float* sums;        // workspace: [splits][M][ldw]
   int64_t ldw;
+  int part_f32;
 };
 // What the workspace has to allow for, and what a call takes.
 EpPlan gated_plan(const GemmParams& p, int backward);

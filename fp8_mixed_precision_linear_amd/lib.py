@@ -566,7 +566,10 @@ def _workspace(ws, need, like, stream):
     if ws is None:
         if stream is not None:
             raise ValueError("a call on an explicit stream needs a workspace")
-        ws = torch.empty(need(), dtype=torch.uint8, device=like.device)
+        n = need()
+        if n == 0:
+            return None, 0, 0
+        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
     elif not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()

@@ -477,3 +477,24 @@ def test_exact_on_each_kernel(L, taken, path, out):
             for h in (0, 1):
                 q, e = G.save(u[:, h * F:(h + 1) * F].float())
                 assert torch.equal(ck.t[:, h * F:(h + 1) * F], q) and torch.equal(exp.t[:, h * nb:(h + 1) * nb], e)
+
+
+@pytest.mark.parametrize("p", [BF, F32])
+@pytest.mark.parametrize("M,K", [(1, 128), (16, 4096), (17, 256), (32, 272), (20, 8192), (33, 256)])
+def test_bias_gradient_of_few_rows(L, M, K, p):
+    """dbias of up to 32 rows has no join; it may start on any element."""
+    F = 203
+    g = gen(M + K)
+    A, sa = operand(g, M, K, 1, 0)
+    B, sb = operand(g, F, K, 0, 0, 0.5 / K ** 0.5)
+    aux = rand(g, (M, 2 * F), 1.5).to(BF)
+    D = torch.empty((M, 2 * F), device="cuda")
+    for first in (0, 1, 3):
+        whole = torch.full((2 * F + 8,), 3.0, dtype=p, device="cuda")
+        db = whole[first:first + 2 * F]
+        say("gated dbias", M, K, p, first)
+        L.fp8_gated_linear(A, 1, 0, sa, B, 0, 0, sb, D, aux=aux, backward=True, dbias=db)
+        torch.cuda.synchronize()
+        o, Eo = G.backward(*R.product(A, 1, 0, sa, B, 0, 0, sb), aux, 4)
+        R.close(db, o.sum(0), Eo.sum(0) + (R.C + M * 2.0 ** -24) * o.abs().sum(0))
+        assert bool((whole[:first] == 3).all()) and bool((whole[first + 2 * F:] == 3).all())
