@@ -10,6 +10,10 @@ training step with delayed scaling, and the same block for single tokens.
                                         way out, FP8 codes and their transpose
     out = h + u W2^T                    FP8 linear: residual on its way out
 
+With --gated, u = silu(g) * w of (g | w) = y1 W1^T + b1 (W1 the gate's rows, then the up
+projection's): one product, which keeps g | w for the backward pass in 8 bits; the
+branch a is kept in 8 bits as well.
+
     python examples/transformer_block.py --tokens 4096 --hidden 4096 --ffn 14336 --heads 32 --kv-heads 8
 """
 import argparse
@@ -69,9 +73,10 @@ class Weight:
 
 
 class Block:
-    def __init__(self, hidden, heads, kv_heads, head_dim, ffn, device="cuda", seed=0):
+    def __init__(self, hidden, heads, kv_heads, head_dim, ffn, device="cuda", seed=0, gated=False):
         self.hidden, self.heads, self.kv, self.dim, self.ffn = hidden, heads, kv_heads, head_dim, ffn
-        self.device = device
+        self.device, self.gated = device, gated
+        self.first = first = 2 * ffn if gated else ffn      # rows of the feed-forward's first product
         g = torch.Generator(device="cpu").manual_seed(seed)
 
         def random(*shape, scale=1.0, mean=0.0):
@@ -81,9 +86,9 @@ class Block:
         self.param = {
             "wqkv": random(wide, hidden, scale=hidden ** -0.5),
             "wo": random(hidden, heads * head_dim, scale=(heads * head_dim) ** -0.5),
-            "w1": random(ffn, hidden, scale=hidden ** -0.5),
+            "w1": random(first, hidden, scale=hidden ** -0.5),
             "w2": random(hidden, ffn, scale=ffn ** -0.5),
-            "b1": random(ffn, scale=0.1), "gate": random(hidden, scale=0.5, mean=0.5),
+            "b1": random(first, scale=0.1), "gate": random(hidden, scale=0.5, mean=0.5),
             "n0": random(hidden, scale=0.1, mean=1.0), "n1": random(hidden, scale=0.1, mean=1.0),
             "na": random(hidden, scale=0.1, mean=1.0),
         }
@@ -133,18 +138,29 @@ class Block:
         L.fp8_block_norm(x, s["a"], s["h"], s["y1"], eps=EPS, w_pre=p["n1"], w_post=p["na"], gate=p["gate"],
                          gate_act=L.GATE_TANH, stats_z=s["sa"], stats_h=s["s1"], y8=y8, y8_scale=scale, y8_amax=amax)
         # the feed-forward pair
-        s["aux"], u8 = self._new(n, self.ffn), self._new(n, self.ffn, dtype=U8)
-        s["u8_t"] = self._new(self.ffn, n, dtype=U8)
+        u8, s["u8_t"] = self._new(n, self.ffn, dtype=U8), self._new(self.ffn, n, dtype=U8)
         uscale, uinv, uamax = self.act["u"]
-        L.fp8_scaled_gemm_ep(y8, L.E4M3, T, inv, q8["w1"].w, L.E4M3, T, q8["w1"].inv, u8, bias=p["b1"],
-                             act=L.ACT_GELU, aux=s["aux"], d_scale=uscale, d_fmt=L.E4M3, D_t=s["u8_t"], d_amax=uamax,
-                             amax_accumulate=True)
+        written = dict(bias=p["b1"], d_scale=uscale, d_fmt=L.E4M3, D_t=s["u8_t"], d_amax=uamax, amax_accumulate=True)
+        if self.gated:
+            s["kept"] = self._checkpoint(n, self.ffn, 2)
+            L.fp8_gated_linear(y8, L.E4M3, T, inv, q8["w1"].w, L.E4M3, T, q8["w1"].inv, u8, act=L.ACT_SILU,
+                               ck=s["kept"][0], ck_exp=s["kept"][1], **written)
+            s["a8"] = self._checkpoint(n, self.hidden)
+            L.fp8_checkpoint_save(s.pop("a"), *s["a8"])
+        else:
+            s["aux"] = self._new(n, self.ffn)
+            L.fp8_scaled_gemm_ep(y8, L.E4M3, T, inv, q8["w1"].w, L.E4M3, T, q8["w1"].inv, u8, act=L.ACT_GELU,
+                                 aux=s["aux"], **written)
         out = self._new(n, self.hidden)
         L.fp8_scaled_gemm_ep(u8, L.E4M3, T, uinv, q8["w2"].w, L.E4M3, T, q8["w2"].inv, out, residual=s["h"])
         # the scales that this step's codes were made with (step() changes them in place)
         s["inv"] = {name: self.act[name][1].clone() for name in self.act.at}
         s["scale"] = {name: self.act[name][0].clone() for name in self.act.at}
         return out, s
+
+    def _checkpoint(self, rows, cols, parts=1):
+        """Room for an 8-bit checkpoint of `parts` matrices side by side: codes, powers of two."""
+        return self._new(rows, parts * cols, dtype=U8), self._new(rows, parts * ((cols + 31) // 32), dtype=U8)
 
     def _cast(self, g, name):
         """E5M2 codes of a gradient and of its transpose, and their inverse scale."""
@@ -172,19 +188,27 @@ class Block:
         # activation on its way out, with the bias gradient
         d8, d8_t, dinv = self._cast(dout, "out")
         g["w2"] = self._wgrad(d8_t, dinv, s["u8_t"], s["inv"]["u"])
-        u8, u8_t = self._new(n, self.ffn, dtype=U8), self._new(self.ffn, n, dtype=U8)
+        u8, u8_t = self._new(n, self.first, dtype=U8), self._new(self.first, n, dtype=U8)
         g["b1"] = torch.empty_like(p["b1"])
         uscale, uinv, uamax = self.grad["u"]
-        L.fp8_scaled_gemm_ep(d8, L.E5M2, T, dinv, q8["w2"].t, L.E4M3, T, q8["w2"].inv, u8, act=L.ACT_GELU,
-                             aux=s["aux"], backward=True, dbias=g["b1"], d_scale=uscale, d_fmt=L.E5M2, D_t=u8_t,
-                             d_amax=uamax, amax_accumulate=True)
+        written = dict(backward=True, dbias=g["b1"], d_scale=uscale, d_fmt=L.E5M2, D_t=u8_t, d_amax=uamax,
+                       amax_accumulate=True)
+        if self.gated:
+            L.fp8_gated_linear(d8, L.E5M2, T, dinv, q8["w2"].t, L.E4M3, T, q8["w2"].inv, u8, act=L.ACT_SILU,
+                               ck=s["kept"][0], ck_exp=s["kept"][1], **written)
+            a = self._new(n, self.hidden)
+            L.fp8_checkpoint_load(*s["a8"], a)
+        else:
+            a = s["a"]
+            L.fp8_scaled_gemm_ep(d8, L.E5M2, T, dinv, q8["w2"].t, L.E4M3, T, q8["w2"].inv, u8, act=L.ACT_GELU,
+                                 aux=s["aux"], **written)
         g["w1"] = self._wgrad(u8_t, uinv, self._transposed(s["y1"], s["scale"]["y1"]), s["inv"]["y1"])
         dy = self._new(n, self.hidden)
         L.fp8_scaled_gemm(u8, L.E5M2, T, uinv, q8["w1"].t, L.E4M3, T, q8["w1"].inv, dy)
         # both norms, the gate and the residual in one pass
         dx, da = self._new(n, self.hidden), self._new(n, self.hidden)
         g["n1"], g["na"], g["gate"] = (torch.empty_like(p["n1"]) for _ in range(3))
-        L.fp8_block_norm_bwd(s["h"], dx, dy=dy, dh=dout, z=s["a"], dz=da, w_pre=p["n1"], w_post=p["na"],
+        L.fp8_block_norm_bwd(s["h"], dx, dy=dy, dh=dout, z=a, dz=da, w_pre=p["n1"], w_post=p["na"],
                              gate=p["gate"], gate_act=L.GATE_TANH, stats_z=s["sa"], stats_h=s["s1"],
                              dw_pre=g["n1"], dw_post=g["na"], dgate=g["gate"])
         # attention
@@ -231,8 +255,8 @@ class Block:
         L.fp8_block_norm(x, a, h, eps=EPS, w_pre=p["n1"], w_post=p["na"], gate=p["gate"], gate_act=L.GATE_TANH,
                          y8=y8, y8_scaling=ROW, y8_scale_inv=inv)
         u = self._new(n, self.ffn)
-        L.fp8_scaled_gemm_ep(y8, L.E4M3, ROW, inv, q8["w1"].w, L.E4M3, T, q8["w1"].inv, u, bias=p["b1"],
-                             act=L.ACT_GELU)
+        first, act = (L.fp8_gated_linear, L.ACT_SILU) if self.gated else (L.fp8_scaled_gemm_ep, L.ACT_GELU)
+        first(y8, L.E4M3, ROW, inv, q8["w1"].w, L.E4M3, T, q8["w1"].inv, u, bias=p["b1"], act=act)
         u8 = self._new(n, self.ffn, dtype=U8)
         L.fp8_cast_rowwise(u, L.E4M3, u8, inv)
         out = self._new(n, self.hidden)
@@ -245,8 +269,9 @@ def main():
     for name, value in (("tokens", 1024), ("hidden", 2048), ("heads", 16), ("kv-heads", 4), ("ffn", 8192),
                         ("steps", 10)):
         ap.add_argument("--" + name, type=int, default=value)
+    ap.add_argument("--gated", action="store_true")
     a = ap.parse_args()
-    b = Block(a.hidden, a.heads, a.kv_heads, a.hidden // a.heads, a.ffn)
+    b = Block(a.hidden, a.heads, a.kv_heads, a.hidden // a.heads, a.ffn, gated=a.gated)
     x = torch.randn(a.tokens, a.hidden, device="cuda").to(BF)
     dout = torch.randn(a.tokens, a.hidden, device="cuda").to(BF)
 
