@@ -93,6 +93,76 @@ __device__ __forceinline__ void codes_of(int fp8, bool tame, const float (&x)[8]
     else encode8<1>(x, lo, hi);
   }
 }
+// The first `bytes` of NW dwords to byte address p, each lane by itself: what lies in
+// whole dwords of memory as those, the ends as bytes and pairs of them.  A tile's few rows
+// wait for instructions, not for memory: with the lanes' exchange of store_row, and
+// partial vectors value by value, 4096 x 4095 x 4096 took 123 us backward instead of 111,
+// 177 forward instead of 174, 1037 x 1999 x 2304 backward 29.8 instead of 27.7 (on rows
+// that start on a dword 26.1 instead of 26.7).
+template <int NW>
+__device__ __forceinline__ void put_words(uint8_t* p, int bytes, const uint32_t (&w)[NW]) {
+  struct __attribute__((packed, aligned(4))) Words { uint32_t v[NW]; };
+  struct __attribute__((packed, aligned(4))) Rest { uint32_t v[NW - 1]; };
+  const uint32_t lead = (0u - (uint32_t)reinterpret_cast<uintptr_t>(p)) & 3u;   // bytes before the first whole dword
+  const bool whole = bytes <= 0 || (bytes == 4 * NW && lead == 0);
+  if (__builtin_amdgcn_ballot_w64(!whole) == 0) {
+    if (bytes > 0) {
+      Words a;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) a.v[k] = w[k];
+      *reinterpret_cast<Words*>(p) = a;
+    }
+    return;
+  }
+  if (bytes <= 0) return;
+  auto ends = [](uint8_t* q, uint32_t n, uint32_t v, bool odd_first) {   // up to three bytes
+    uint32_t at = 0;
+    if (odd_first && (n & 1)) { *q = (uint8_t)v; at = 1; }
+    if (n & 2) { *reinterpret_cast<uint16_t*>(q + at) = (uint16_t)(v >> (8 * at)); at += 2; }
+    if (!odd_first && (n & 1)) q[at] = (uint8_t)(v >> (8 * at));
+  };
+  const int first = (int)lead < bytes ? (int)lead : bytes, rest = bytes - first;
+  uint8_t* q = p + first;
+  uint32_t a[NW];
+#pragma unroll
+  for (int k = 0; k < NW; ++k) a[k] = __builtin_amdgcn_alignbyte(k + 1 < NW ? w[k + 1] : 0u, w[k], lead);
+  ends(p, (uint32_t)first, w[0], lead == (uint32_t)first);
+  if (bytes == 4 * NW) {   // (not aligned, so one dword is left of its own)
+    Rest b;
+#pragma unroll
+    for (int k = 0; k < NW - 1; ++k) b.v[k] = a[k];
+    *reinterpret_cast<Rest*>(q) = b;
+    if (lead == 0) reinterpret_cast<uint32_t*>(q)[NW - 1] = a[NW - 1];
+    else ends(q + 4 * (NW - 1), 4 - lead, a[NW - 1], false);
+  } else {
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      if (4 * k + 4 <= rest) reinterpret_cast<uint32_t*>(q)[k] = a[k];
+      else if (4 * k < rest) ends(q + 4 * k, (uint32_t)(rest - 4 * k), a[k], false);
+    }
+  }
+}
+// Eight bf16 or binary32 values, or eight codes, to p; n: how many are written.
+template <bool FAST>
+__device__ __forceinline__ void put_values(void* p, int f32, int n, const float (&v)[8]) {
+  if (FAST || f32) {
+    put8<16, FAST>(p, f32, n, v);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+    put_words<4>(reinterpret_cast<uint8_t*>(p), 2 * n, w);
+  }
+}
+template <bool FAST>
+__device__ __forceinline__ void put_codes(uint8_t* p, int n, uint32_t lo, uint32_t hi) {
+  if constexpr (FAST) {
+    put8_codes<16, true>(p, n, lo, hi);
+  } else {
+    const uint32_t w[2] = {lo, hi};
+    put_words<2>(p, n, w);
+  }
+}
 // Code k to the top of column k's word, the rows before down a byte.
 __device__ __forceinline__ void turn(uint32_t (&turned)[8], uint32_t lo, uint32_t hi) {
 #pragma unroll
@@ -261,8 +331,8 @@ struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
       }
       if (e.aux) {
         uint16_t* a = reinterpret_cast<uint16_t*>(e.aux) + m * e.ldaux + c;
-        put8<LPR, FAST>(a, 0, n, g);
-        put8<LPR, FAST>(a + F, 0, n, u);
+        put_values<FAST>(a, 0, n, g);
+        put_values<FAST>(a + F, 0, n, u);
       }
       if constexpr (KEEPS) {
         if (e.ck) {
@@ -278,10 +348,10 @@ struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
       uint32_t lo, hi;
       this->see(v, n, lo, hi);
       if constexpr (OUT8) {
-        put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
+        put_codes<FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
         if (p.D_t) turn(turned, lo, hi);
       } else {
-        put8<LPR, FAST>(d, p.d_f32, n, v);
+        put_values<FAST>(d, p.d_f32, n, v);
       }
       d += p.ldd * esz;
     }
@@ -308,7 +378,7 @@ struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
       for (int k = 0; k < 8; ++k) x[k] = v[k] * ck_scale(byte);
       encode8<0>(x, lo, hi);
     }
-    put8_codes<LPR, FAST>(ck, n, lo, hi);
+    put_codes<FAST>(ck, n, lo, hi);
     if ((cq & 3) == 0 && n > 0) *exp = (uint8_t)byte;
   }
 
@@ -391,19 +461,36 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
   }
   static __device__ __forceinline__ void load_codes(const uint8_t* a, int n, Eight& w) {
     if (n <= 0) return;
-    if (FAST || n >= 8) {
-      struct __attribute__((packed, aligned(FAST ? 4 : 1))) Two { uint32_t a, b; };
+    if constexpr (FAST) {
+      struct __attribute__((packed, aligned(4))) Two { uint32_t a, b; };
       const Two q = *reinterpret_cast<const Two*>(a);
       w[0] = q.a;
       w[1] = q.b;
-    } else {
-      uint32_t d[2] = {0u, 0u};
-#pragma unroll
-      for (int k = 0; k < 7; ++k)
-        if (k < n) d[k >> 2] |= (uint32_t)a[k] << (8 * (k & 3));
-      w[0] = d[0];
-      w[1] = d[1];
+    } else {   // the dwords of memory that hold one of them (see codes())
+      const int o = (int)(reinterpret_cast<uintptr_t>(a) & 3u);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(a - o);
+      struct __attribute__((packed, aligned(4))) Two { uint32_t a, b; };
+      w[1] = w[2] = 0u;
+      if (o + n > 4) {
+        const Two t = *reinterpret_cast<const Two*>(q);
+        w[0] = t.a;
+        w[1] = t.b;
+      } else {
+        w[0] = q[0];
+      }
+      if (o + n > 8) w[2] = q[2];
     }
+  }
+  // The n codes at a out of the dwords that load_codes took.
+  static __device__ __forceinline__ uint2 codes(const Eight& w, const uint8_t* a, int n) {
+    if constexpr (FAST) return make_uint2(w[0], w[1]);
+    const uint32_t o = (uint32_t)reinterpret_cast<uintptr_t>(a);   // (alignbyte takes its two lowest bits)
+    uint32_t lo = __builtin_amdgcn_alignbyte(w[1], w[0], o), hi = __builtin_amdgcn_alignbyte(w[2], w[1], o);
+    if (n < 8) {
+      lo = n >= 4 ? lo : (n <= 0 ? 0u : lo & (0xFFFFFFFFu >> (32 - 8 * n)));
+      hi = n <= 4 ? 0u : hi & (0xFFFFFFFFu >> (64 - 8 * n));
+    }
+    return make_uint2(lo, hi);
   }
   // Each lane's own words: 16 bytes of g's eight values and 16 of u's a row, or 16 of
   // both's codes and exponents.
@@ -412,7 +499,11 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
 #pragma unroll
     for (int t = 0; t < RPL; ++t) {
       if (coded()) {
-        q[t * 64] = make_uint4(o[t].g[0], o[t].g[1], o[t].u[0], o[t].u[1]);
+        const int64_t m = m0 + rg * RPL + t;
+        const uint8_t* a = e.ck + m * e.ldck + c;
+        const int n = m < p.M ? nv : 0;
+        const uint2 g = codes(o[t].g, a, n), u = codes(o[t].u, a + p.N, n);
+        q[t * 64] = make_uint4(g.x, g.y, u.x, u.y);
         reinterpret_cast<uint32_t*>(ol + RPL * 64 * 16)[t * 64 + lane] = o[t].xg | (o[t].xu << 8);
       } else {
         const uint16_t* a = reinterpret_cast<const uint16_t*>(e.aux) + (m0 + rg * RPL + t) * e.ldaux + c;
@@ -475,17 +566,17 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
       uint32_t lo, hi;
       this->see(g, n, lo, hi);
       if constexpr (OUT8) {
-        put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
+        put_codes<FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
         if (p.D_t) turn(tg, lo, hi);
       } else {
-        put8<LPR, FAST>(d, p.d_f32, n, g);
+        put_values<FAST>(d, p.d_f32, n, g);
       }
       this->see(u, n, lo, hi);
       if constexpr (OUT8) {
-        put8_codes<LPR, FAST>(reinterpret_cast<uint8_t*>(d) + half, n, lo, hi);
+        put_codes<FAST>(reinterpret_cast<uint8_t*>(d) + half, n, lo, hi);
         if (p.D_t) turn(tu, lo, hi);
       } else {
-        put8<LPR, FAST>(d + half, p.d_f32, n, u);
+        put_values<FAST>(d + half, p.d_f32, n, u);
       }
       d += p.ldd * esz;
     }
