@@ -201,6 +201,19 @@ __device__ __forceinline__ void put_columns(uint8_t* d_t, int64_t ldt, const uin
   }
 }
 
+// A wavefront's largest |d|, and the row and first of n columns where a lane met it (see
+// k_gated_amax).
+__device__ __forceinline__ void put_key(const GatedParams& e, float top, int row, int col, int n) {
+  const uint32_t b = __float_as_uint(top), m = wave_max(b);
+  const int at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(b == m));
+  const uint32_t r = lane_u32((uint32_t)row, at), c = lane_u32((uint32_t)col, at);
+  const int64_t wg = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if ((threadIdx.x & 63) == 0) {   // (c is a multiple of 8)
+    e.keys[wg * e.key_waves + (threadIdx.x >> 6)] = m;
+    e.key_at[wg * e.key_waves + (threadIdx.x >> 6)] = make_uint2(r, c | (n == 16 ? 1u : 0u));
+  }
+}
+
 // What both directions share: WTN columns in LDS, OC of them outputs of the wavefront,
 // lane's outputs c .. c + 7, RPL rows of a strip per lane (lanes past the strip's 16
 // rows are idle: on).  FAST as in gemm_ep.h.
@@ -295,6 +308,7 @@ struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
   static constexpr int src_at = 64 * WTN, codes_at = src_at;
   static constexpr int bytes(int TI) { return codes_at + (OUT8 ? OC * (16 * TI + 16) : 0); }
   float bias[2][8];
+  int where = 0;         // the row of the lane's largest |d|
 
   __device__ __forceinline__ GatedWave(const GemmParams& p_, const GatedParams& e_, int64_t n0, int lane_)
       : Base(p_, e_, n0 / 2, lane_) {
@@ -346,8 +360,10 @@ struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] *= u[k];
       uint32_t lo, hi;
+      const float before = this->top;
       this->see(v, n, lo, hi);
       if constexpr (OUT8) {
+        where = __float_as_uint(this->top) != __float_as_uint(before) ? (int)m : where;
         put_codes<FAST>(reinterpret_cast<uint8_t*>(d), n, lo, hi);
         if (p.D_t) turn(turned, lo, hi);
       } else {
@@ -404,7 +420,13 @@ struct GatedWave : GatedBase<WTN, WTN / 2, OUT8, FAST> {
     const int64_t first = n0 / 2, cols = p.N - first;
     put_columns<TS, ROWS>(p.D_t, p.ldt, tl, lane, first, cols < OC ? (int)cols : OC, r0, p.M - r0);
   }
-  __device__ __forceinline__ void put_dbias(int64_t) {}
+  // (what a backward wavefront has to leave at its end, a forward one has not: the key of
+  // its largest |d|)
+  __device__ __forceinline__ void put_dbias(int64_t) {
+    if constexpr (OUT8) {
+      if (e.keys) put_key(e, this->top, where, (int)c, 8);
+    }
+  }
 };
 
 // Backward: WTN columns are as many outputs of each half.  KEPT: g and u come from BF16

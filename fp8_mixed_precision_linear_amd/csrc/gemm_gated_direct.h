@@ -229,11 +229,15 @@ struct GatedRun {
 
   template <typename Deq>
   __device__ __forceinline__ void finish(const v4f (&acc)[TI][TJ], Deq&& deq, int64_t, int lane, int wave) const {
-    const float top = rows > 0 ? body(acc, deq) : 0.0f;
+    int where = 0;
+    const float top = rows > 0 ? body(acc, deq, where) : 0.0f;
+    if constexpr (OUT8) {
+      if (e.keys) put_key(e, top, (int)r0 + where, (int)c0 + (int)col, N);
+    }
     if (p.d_amax) ep_amax<NW>(p.d_amax, amax_bits<OUT8>(p, top), lane, wave);
   }
   template <typename Deq>
-  __device__ __forceinline__ float body(const v4f (&acc)[TI][TJ], Deq&& deq) const {
+  __device__ __forceinline__ float body(const v4f (&acc)[TI][TJ], Deq&& deq, int& where) const {
     const int64_t F = p.N;
     const int esz = OUT8 ? 1 : (p.d_f32 ? 4 : 2);
     const RowsOf D(p.D, r0, p.ldd * esz, rows), aux(e.aux, r0, e.ldaux * 2, rows), ck(e.ck, r0, e.ldck, rows),
@@ -286,6 +290,7 @@ struct GatedRun {
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] *= U[k];
         const float m = row < rows && on ? max_of(v) : 0.0f;
+        if constexpr (OUT8) where = __float_as_uint(__builtin_elementwise_maximum(top, m)) != __float_as_uint(top) ? row : where;
         top = __builtin_elementwise_maximum(top, m);
         const uint32_t off = on ? (uint32_t)(row * D.ld) + c * (uint32_t)esz : kOOB;
         if constexpr (OUT8) {

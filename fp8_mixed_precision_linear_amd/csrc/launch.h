@@ -236,6 +236,9 @@ struct GatedParams {
   float* sums;        // workspace: [splits][M][ldw]
   int64_t ldw;
   int part_f32;
+  uint32_t* keys;     // forward with FP8 output and an amax (workspace): see k_gated_amax
+  uint2* key_at;
+  int key_waves;      // wavefronts of a workgroup that write one
 };
 // What the workspace has to allow for, and what a call takes.
 EpPlan gated_plan(const GemmParams& p, int backward);

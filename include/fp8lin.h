@@ -665,7 +665,9 @@ fp8_status fp8_scaled_gemm_ep_plan(const fp8_gemm_args* gemm, const fp8_epilogue
  *     dbias[2 F] = column sums of D before its rounding.
  * D is BF16, FP32 or FP8 codes of d_scale times it (backward: one scale for
  * both halves) with the transposed copy D_t ([F][ldt]; backward [2 F][ldt]);
- * d_amax as in fp8_scaled_gemm.  With codes in both orders, D and D_t of a
+ * d_amax as in fp8_scaled_gemm; of a forward call with FP8 output it is the largest
+ * output summed again in binary32, apart from the matrix unit's cut (whose D it may
+ * exceed or miss by some 1e-5 of itself).  With codes in both orders, D and D_t of a
  * backward call are the operands of the products that follow, each one product
  * over 2 F: the input's gradient (K = 2 F) and the weights' (2 F rows).
  *   a_fmt     FP8_E4M3; backward also FP8_E5M2.   b_fmt  FP8_E4M3.
@@ -680,7 +682,7 @@ fp8_status fp8_scaled_gemm_ep_plan(const fp8_gemm_args* gemm, const fp8_epilogue
  *   ck        [M][ldck] E4M3 codes, 2 F columns, and ck_exp [M][ldexp], 2 ceil(F /
  *             32) bytes: g's and u's as fp8_checkpoint_save writes each.
  *   workspace fp8_gated_linear_workspace(M, F, K, a_scaling, b_scaling, backward)
- *             bytes.
+ *             bytes; calls that may run at the same time need one each.
  * No output may overlap an input.  K == 0 is a sum of nothing; M == 0 sets dbias
  * to 0.
  * Errors: as fp8_scaled_gemm, and FP8_ERR_ARG (backward, act, param_dtype; a
