@@ -3,7 +3,9 @@
 //
 // A lane takes eight neighbouring columns of a row, four lanes a block of 32, whose
 // largest magnitude they exchange inside their quad; nothing is kept but the eight
-// values.  Bound: HBM.
+// values.  Bound: HBM (8192 x 8192 BF16 saved in 40.5 us, 5.0 TB/s, a copy's rate; 8192 x 14336
+// loaded in 63), small ones by a launch and a load's latency (1531 x 2053 FP32 7.4 us, of
+// which the call's host part is 5.5).  A row per workgroup and step: no lane has a division.
 #include "checkpoint.h"
 #include "launch.h"
 

@@ -64,8 +64,9 @@ hipError_t launch_join(const GemmParams& p, const GatedParams& e, hipStream_t s)
 // outputs among which a lane met it) in place of an atomic maximum, and this workgroup
 // takes the largest key's outputs again in binary32, 32 lanes to a sum.  Equal keys: the
 // first.  Infinities, NaN and zeros stay as they are.
-// Bound by latency, a chain of six loads: 5.7 us at K = 256, 7.6 at 4096, 10.6 at 4096 with block scales (a call's
-// time grows by 2 us where it was the host's, by 17 of 2710 at 8192 x 28672 x 8192).
+// Bound by latency, a chain of six loads: 5.7 us at K = 256, 7.6 at 4096, 10.6 at 4096 with
+// block scales, 15 at 8192 x 28672 x 8192 (14 336 keys).  A call's time grows by 2 us where it
+// was the host's, by 17 of 2710 there.
 constexpr int AMAX_THREADS = 1024;
 __device__ __forceinline__ float scale_at(const float* s, int scaling, int64_t rows, int64_t kb, int64_t row) {
   if (scaling == 1 || scaling == 3) return s[kb * rows + row];

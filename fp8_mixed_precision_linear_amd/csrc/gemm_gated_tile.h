@@ -1,7 +1,9 @@
 // gemm_gated_tile.h -- the tile kernels (gemm_ep_tile.h) with the gated pair's epilogue;
 // instantiated by gemm_gated_tile.hip, gemm_gated_grad_tile.hip and, for promoted block
 // scales, their _blk twins.  Forward both operands are E4M3; backward the gradient may be
-// E5M2 or E4M3, the weights are E4M3.
+// E5M2 or E4M3, the weights are E4M3.  777 x 1999 x 2304 with power-of-two scales takes 22.3 us
+// forward, 1037 rows 27.6 backward: a step of K 0.59, the rest launch, first loads and
+// epilogue.
 #pragma once
 
 #include "gemm_ep_tile.h"

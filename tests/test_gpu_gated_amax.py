@@ -93,3 +93,23 @@ def test_amax_without_rows_or_k(L):
                            torch.zeros((2 * F, K), dtype=U8, device="cuda"), 0, 0, one if K else None,
                            torch.empty((M, F), dtype=U8, device="cuda"), act=L.ACT_NONE, bias=bias, d_fmt=L.E4M3, d_scale=scale, d_amax=amax)
         assert float(amax) == want
+
+
+def test_two_streams_add_to_one_amax(L):
+    """Two calls at once, each with a workspace of its own, and the larger of their amaxes."""
+    M, F, K = 300, 520, 1024
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    scale = torch.full((1,), 2.0 ** -24, device="cuda")
+    amax, each = torch.zeros(1, device="cuda"), torch.zeros(2, device="cuda")
+    ops = [planted(M, F, K, (0, 0), (7, 11), s) for s in (1, 2)]
+    ws = [torch.empty(L.fp8_gated_linear_workspace(M, F, K, 0, 0), dtype=U8, device="cuda") for _ in range(2)]
+    D = [torch.empty((M, F), dtype=U8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (A, sa, B, sb), w, d, s in zip(ops, ws, D, streams):
+            L.fp8_gated_linear(A, 0, 0, sa, B, 0, 0, sb, d, d_fmt=L.E4M3, d_scale=scale, d_amax=amax, amax_accumulate=True,
+                               workspace=w, stream=s)
+    for i, ((A, sa, B, sb), w, d, s) in enumerate(zip(ops, ws, D, streams)):
+        L.fp8_gated_linear(A, 0, 0, sa, B, 0, 0, sb, d, d_fmt=L.E4M3, d_scale=scale, d_amax=each[i:i + 1], workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert float(amax) == float(each.max()) > 0
