@@ -562,6 +562,9 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
       const int n = first + t < p.M ? nv : 0;
       float v[8], g[8], u[8], a[8], s[8];
       read8(wl, rg * RPL + t, 2 * cq, v);
+      // (past the last row stand zeros; times an infinite scale they are NaN)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = n > 0 ? v[k] : 0.0f;
       const uint4 x = q[t * 64];
       if (coded()) {
         const uint32_t b = reinterpret_cast<const uint32_t*>(ol + RPL * 64 * 16)[t * 64 + lane];
@@ -577,7 +580,7 @@ struct GatedGradWave : GatedBase<WTN, WTN, OUT8, FAST> {
         g[k] = v[k] * u[k] * s[k];
         u[k] = v[k] * a[k];
       }
-      // (rows past the last and columns past the last have g = u = 0: see fetch)
+      // (rows past the last have v = g = u = 0, columns past the last are not stored)
       if (e.dbias) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {

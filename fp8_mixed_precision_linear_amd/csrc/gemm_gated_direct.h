@@ -441,14 +441,14 @@ struct GatedGradRun {
               for (int q = 0; q < 4; ++q) v[4 * j + q] = deq(i0 + t, j0 + E / 4 * i + j, q, x[q]);
             }
           });
-          // (an infinity of A's row times the zeros past B's last one is a NaN)
+          // (past the last row and column stand zeros, and an infinity times a zero is a NaN)
 #pragma unroll
-          for (int k = 0; k < E; ++k) v[k] = there ? v[k] : 0.0f;
+          for (int k = 0; k < E; ++k) v[k] = there && row < rows ? v[k] : 0.0f;
           kept(in4[t], i, G, U);
           __builtin_amdgcn_sched_barrier(0);
           if (i == N / E - 1) load(unit + 1, t);
           __builtin_amdgcn_sched_barrier(0);
-          // (rows past the last have g = u = 0: no sum or maximum needs a mask)
+          // (rows and columns past the last have v = g = u = 0: no sum or maximum needs a mask)
           act_and_slope(e.act, G, a, s);
 #pragma unroll
           for (int k = 0; k < E; ++k) {

@@ -72,3 +72,45 @@ def test_infinite_gradient(L, taken, path, kept, out):
     assert amax == INF
     assert int((db == INF).sum()) == db.numel()
     assert taken == [path[4:7]]
+
+
+@pytest.mark.parametrize("path", [p for p in PATHS if p[3][0] == 5])
+@pytest.mark.parametrize("kept", ["bf16", "ckpt"])
+@pytest.mark.parametrize("out", ["bf16", "e5m2"])
+def test_infinite_scale_of_the_last_row(L, taken, path, kept, out):
+    """The rows past the last have no scale of their own."""
+    def change(A, sa, sb):
+        sa[-1] = INF
+    D, amax, db = call(L, path, kept, out, change)
+    if out == "bf16":
+        assert bool((D[-1] == INF).all()) and bool(D[:-1].isfinite().all())
+    else:
+        assert bool((D[-1] == 0x7B).all())
+    assert amax == INF
+    assert int((db == INF).sum()) == db.numel()
+    assert taken == [path[4:7]]
+
+
+@pytest.mark.parametrize("path", [p for p in PATHS if p[3][1] != 4])      # (powers of two are finite)
+@pytest.mark.parametrize("kept", ["bf16", "ckpt"])
+@pytest.mark.parametrize("out", ["bf16", "e5m2"])
+def test_infinite_scale_of_weights(L, taken, path, kept, out):
+    """Of all of them, of one column or of one block's: its columns are infinite, and their sums."""
+    F, bsc = path[1], path[3][1]
+    bad = torch.zeros(F, dtype=torch.bool, device="cuda")
+    bad[slice(None) if bsc == 0 else slice(7, 8) if bsc == 5 else slice(128, 256)] = True
+    bad = bad.repeat(2)
+
+    def change(A, sa, sb):
+        if bsc in (2, 4):
+            sb[1, 1] = INF
+        else:
+            sb[7 if bsc == 5 else 0] = INF
+    D, amax, db = call(L, path, kept, out, change)
+    if out == "bf16":
+        assert bool((D[:, bad] == INF).all()) and bool(D[:, ~bad].isfinite().all())
+    else:
+        assert bool((D[:, bad] == 0x7B).all())
+    assert amax == INF
+    assert int((db[bad] == INF).sum()) == int(bad.sum()) and bool(db[~bad].isfinite().all())
+    assert taken == [path[4:7]]
