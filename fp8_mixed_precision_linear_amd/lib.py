@@ -200,6 +200,21 @@ def _stream(stream):
     return int(stream)
 
 
+def _stream_on(dev, stream):
+    """_stream of a call whose tensors are on GPU dev: the current device, where the
+    launch goes, and an explicit stream's."""
+    here = torch._C._cuda_getDevice()
+    if dev != here:
+        raise ValueError(f"the operands are on cuda:{dev}, the current device is cuda:{here}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(here)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != here:
+            raise ValueError(f"the stream is of cuda:{stream.device_index}, the operands are on cuda:{here}")
+        return stream.cuda_stream
+    return int(stream)
+
+
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I64 = (torch.int64,)
@@ -481,25 +496,28 @@ _pack_gated = _packer("iiiPPqPqPqPPq", GatedArgs)
 _pack_rope = _packer("qqqqqiiifPPiqPqqPqqPqqPqq", RopeArgs)
 
 
-def _refuse(t, want, dtype, name):
-    """What is wrong with a tensor that should have been [want] of dtype."""
+def _refuse(t, want, dtype, name, dev=None):
+    """What is wrong with a tensor that should have been [want] of dtype, on GPU dev."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's first operand on cuda:{dev}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     raise ValueError(f"{name} must be {tuple(want)} with rows of unit stride that do not overlap, got "
                      f"{tuple(t.shape)}, strides {t.stride()}")
 
 
-def _mat(t, shape, dtype, name):
+def _mat(t, shape, dtype, name, dev=None):
     """(pointer, row stride) of a 2-D GPU tensor of that shape and type, whose
-    rows may be strided; (0, columns) for None."""
+    rows may be strided; (0, columns) for None.  dev: the GPU that it has to be on
+    (None: any)."""
     if t is None:
         return 0, shape[1]
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda:
-        _refuse(t, shape, dtype, name)
+    if t.dtype != dtype or t.shape != shape or (not t.is_cuda if dev is None else not 0 <= dev == t.get_device()):
+        _refuse(t, shape, dtype, name, dev)
     if t.is_contiguous():
         return t.data_ptr(), shape[1]
     ld, one = t.stride()
@@ -510,28 +528,28 @@ def _mat(t, shape, dtype, name):
     return t.data_ptr(), ld
 
 
-def _codes(t, shape, name):
+def _codes(t, shape, name, dev=None):
     """_mat of FP8 codes (uint8 or a float8 type)."""
     if t is not None and t.dtype not in _U8:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_U8}")
-    return _mat(t, shape, None if t is None else t.dtype, name)
+    return _mat(t, shape, None if t is None else t.dtype, name, dev)
 
 
-def _vec(t, n, dtype, name):
+def _vec(t, n, dtype, name, dev=None):
     """Pointer of a contiguous 1-D GPU tensor of n elements (None -> 0)."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_cuda or not t.is_contiguous():
-        _refuse(t, (n,), dtype, name)
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (not t.is_cuda if dev is None else not 0 <= dev == t.get_device()) or not t.is_contiguous():
+        _refuse(t, (n,), dtype, name, dev)
     return t.data_ptr()
 
 
-def _floats(t, n, name):
+def _floats(t, n, name, dev=None):
     """Pointer of a contiguous float32 GPU tensor of at least n elements."""
     if t is None:
         return 0
-    if t.dtype != _FLOAT or not t.is_cuda or not t.is_contiguous():
-        _refuse(t, (n,), _FLOAT, name)
+    if t.dtype != _FLOAT or (not t.is_cuda if dev is None else not 0 <= dev == t.get_device()) or not t.is_contiguous():
+        _refuse(t, (n,), _FLOAT, name, dev)
     if t.numel() < n:
         _need(t, n, name)
     return t.data_ptr()
@@ -561,7 +579,7 @@ def _gate(gate, shape, ptype, name="gate"):
     return (GATE_FULL, *_mat(gate, shape, _BFLOAT, name))
 
 
-def _workspace(ws, need, like, stream):
+def _workspace(ws, need, like, stream, dev=None):
     """(tensor, pointer, bytes) of the caller's workspace, or of one from
     torch's allocator (on the current stream only, whose order keeps it)."""
     if ws is None:
@@ -571,8 +589,8 @@ def _workspace(ws, need, like, stream):
         if n == 0:
             return None, 0, 0
         ws = torch.empty(n, dtype=torch.uint8, device=like.device)
-    elif not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous GPU tensor")
+    elif not ws.is_cuda or not ws.is_contiguous() or (dev is not None and ws.get_device() != dev):
+        raise ValueError("workspace must be a contiguous GPU tensor, on the operands' device")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -661,10 +679,10 @@ def fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling) -> int:
     return _L.fp8_scaled_gemm_ep_workspace(M, N, K, a_scaling, b_scaling)
 
 
-def _scales(t, scaling, rows, nkb, name):
+def _scales(t, scaling, rows, nkb, name, dev=None):
     n = (1 if scaling == SCALE_TENSOR else rows if scaling == SCALE_ROW else
          nkb * (rows if scaling in (SCALE_1x128, SCALE_1x128_POW2) else (rows + 127) // 128))
-    return _floats(t, n if nkb > 0 else 0, name)
+    return _floats(t, n if nkb > 0 else 0, name, dev)
 
 
 _OUT = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
@@ -732,7 +750,7 @@ def fp8_gated_linear(A, a_fmt, a_scaling, a_scale_inv, B, b_fmt, b_scaling, b_sc
     transposed D_t).  g beside u are kept by the forward call, and read by the
     backward one, as aux [M][2F] bf16 or as ck [M][2F] codes with ck_exp
     [M][2 ceil(F / 32)] (see fp8_checkpoint_save).  All but the scales, biases and D_t
-    may have strided rows."""
+    may have strided rows.  Every tensor is on the current device."""
     M, K = A.shape
     rows = B.shape[0]
     if backward:
@@ -754,58 +772,60 @@ def fp8_gated_linear(A, a_fmt, a_scaling, a_scale_inv, B, b_fmt, b_scaling, b_sc
     pt = _param_type(bias, dbias)
     kept = torch.Size((M, 2 * F))
     nkb = (K + 127) // 128 if M > 0 and F > 0 else 0
-    ap, lda = _codes(A, A.shape, "A")
-    bp, ldb = _codes(B, torch.Size((rows, K)), "B")
-    dp, ldd = _mat(D, mn, dt, "D")
-    tp, ldt = _codes(D_t, torch.Size((n, M)), "D_t") if D_t is not None else (0, M)
+    on = A.get_device()
+    ap, lda = _codes(A, A.shape, "A", on)
+    bp, ldb = _codes(B, torch.Size((rows, K)), "B", on)
+    dp, ldd = _mat(D, mn, dt, "D", on)
+    tp, ldt = _codes(D_t, torch.Size((n, M)), "D_t", on) if D_t is not None else (0, M)
     ws, wp, wn = _workspace(workspace, lambda: fp8_gated_linear_workspace(M, F, K, a_scaling, b_scaling, backward), A,
-                            stream)
-    g = _pack_gemm(M, F, K, lda, ldb, ldd, ap, a_fmt, a_scaling, _scales(a_scale_inv, a_scaling, M, nkb, "a_scale_inv"),
-                   bp, b_fmt, b_scaling, _scales(b_scale_inv, b_scaling, rows, nkb, "b_scale_inv"), dp, d_dtype,
-                   _floats(d_amax, 1, "d_amax"), 0, _floats(d_scale, 1, "d_scale"), tp, ldt,
+                            stream, on)
+    g = _pack_gemm(M, F, K, lda, ldb, ldd, ap, a_fmt, a_scaling, _scales(a_scale_inv, a_scaling, M, nkb, "a_scale_inv", on),
+                   bp, b_fmt, b_scaling, _scales(b_scale_inv, b_scaling, rows, nkb, "b_scale_inv", on), dp, d_dtype,
+                   _floats(d_amax, 1, "d_amax", on), 0, _floats(d_scale, 1, "d_scale", on), tp, ldt,
                    1 if amax_accumulate else 0)
-    e = _pack_gated(1 if backward else 0, act, _DT[pt], _vec(bias, 2 * F, pt, "bias"), *_mat(aux, kept, _BFLOAT, "aux"),
-                    *_codes(ck, kept, "ck"), *_bytes(ck_exp, torch.Size((M, 2 * ((F + 31) // 32))), "ck_exp"),
-                    _vec(dbias, 2 * F, pt, "dbias"), wp, wn)
-    status = _L.fp8_gated_linear(g, e, _stream(stream))
+    e = _pack_gated(1 if backward else 0, act, _DT[pt], _vec(bias, 2 * F, pt, "bias", on), *_mat(aux, kept, _BFLOAT, "aux", on),
+                    *_codes(ck, kept, "ck", on), *_bytes(ck_exp, torch.Size((M, 2 * ((F + 31) // 32))), "ck_exp", on),
+                    _vec(dbias, 2 * F, pt, "dbias", on), wp, wn)
+    status = _L.fp8_gated_linear(g, e, _stream_on(on, stream))
     if status:
         _check("fp8_gated_linear", status)
 
 
-def _bytes(t, shape, name):
+def _bytes(t, shape, name, dev):
     """_mat of a checkpoint's powers of two (uint8 or float8_e8m0fnu)."""
     if t is not None and t.dtype not in _POWERS:
         raise TypeError(f"{name} has dtype {t.dtype}, expected uint8 or float8_e8m0fnu")
-    return _mat(t, shape, None if t is None else t.dtype, name)
+    return _mat(t, shape, None if t is None else t.dtype, name, dev)
 
 
 def _checkpoint(x, ck, ck_exp, name):
     rows, cols = shape = _two_dim(x, name)
     if ck is None or ck_exp is None:
         raise ValueError("ck and ck_exp are required")
-    nb = (cols + 31) // 32
-    if (ck.shape == shape and ck_exp.shape == (rows, nb) and ck.dtype in _U8 and ck_exp.dtype in _POWERS and x.is_cuda
-            and ck.is_cuda and ck_exp.is_cuda and x.is_contiguous() and ck.is_contiguous() and ck_exp.is_contiguous()):
+    nb, on = (cols + 31) // 32, x.get_device()
+    if (ck.shape == shape and ck_exp.shape == (rows, nb) and ck.dtype in _U8 and ck_exp.dtype in _POWERS
+            and 0 <= on == ck.get_device() == ck_exp.get_device() and x.is_contiguous() and ck.is_contiguous()
+            and ck_exp.is_contiguous()):
         # (what most calls are; a small matrix's call is the host's time)
-        return rows, cols, x.data_ptr(), cols, ck.data_ptr(), cols, ck_exp.data_ptr(), nb
-    return (rows, cols, *_mat(x, shape, x.dtype, name), *_codes(ck, shape, "ck"),
-            *_bytes(ck_exp, torch.Size((rows, nb)), "ck_exp"))
+        return on, rows, cols, x.data_ptr(), cols, ck.data_ptr(), cols, ck_exp.data_ptr(), nb
+    return (on, rows, cols, *_mat(x, shape, x.dtype, name, on), *_codes(ck, shape, "ck", on),
+            *_bytes(ck_exp, torch.Size((rows, nb)), "ck_exp", on))
 
 
 def fp8_checkpoint_save(x, ck, ck_exp, stream=None):
     """x [rows][cols], bf16 or float32, kept for the backward pass in 8 bits: ck
     [rows][cols] E4M3 codes (uint8 or float8) and ck_exp [rows][ceil(cols / 32)] one
     power of two for each 32 columns (uint8, or float8_e8m0fnu).  Rows may be strided."""
-    rows, cols, xp, ldx, cp, ldc, ep, lde = _checkpoint(x, ck, ck_exp, "x")
-    status = _L.fp8_checkpoint_save(xp, _DT[x.dtype], rows, cols, ldx, cp, ldc, ep, lde, _stream(stream))
+    on, rows, cols, xp, ldx, cp, ldc, ep, lde = _checkpoint(x, ck, ck_exp, "x")
+    status = _L.fp8_checkpoint_save(xp, _DT[x.dtype], rows, cols, ldx, cp, ldc, ep, lde, _stream_on(on, stream))
     if status:
         _check("fp8_checkpoint_save", status)
 
 
 def fp8_checkpoint_load(ck, ck_exp, y, stream=None):
     """y [rows][cols], bf16 or float32: the values of a checkpoint."""
-    rows, cols, yp, ldy, cp, ldc, ep, lde = _checkpoint(y, ck, ck_exp, "y")
-    status = _L.fp8_checkpoint_load(cp, ldc, ep, lde, rows, cols, yp, _DT[y.dtype], ldy, _stream(stream))
+    on, rows, cols, yp, ldy, cp, ldc, ep, lde = _checkpoint(y, ck, ck_exp, "y")
+    status = _L.fp8_checkpoint_load(cp, ldc, ep, lde, rows, cols, yp, _DT[y.dtype], ldy, _stream_on(on, stream))
     if status:
         _check("fp8_checkpoint_load", status)
 

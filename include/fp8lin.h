@@ -684,7 +684,7 @@ fp8_status fp8_scaled_gemm_ep_plan(const fp8_gemm_args* gemm, const fp8_epilogue
  *   workspace fp8_gated_linear_workspace(M, F, K, a_scaling, b_scaling, backward)
  *             bytes; calls that may run at the same time need one each.
  * No output may overlap an input.  K == 0 is a sum of nothing; M == 0 sets dbias
- * to 0.
+ * to 0.  Every pointer is memory of the current device, and the stream is one of its.
  * Errors: as fp8_scaled_gemm, and FP8_ERR_ARG (backward, act, param_dtype; a
  * bias in a backward call, dbias in a forward one; aux and ck both in a backward
  * one), FP8_ERR_NULL (one of ck and ck_exp alone; neither aux nor ck in a backward call;
@@ -723,7 +723,8 @@ fp8_status fp8_gated_linear_plan(const fp8_gemm_args* gemm, const fp8_gated_args
  *   x, y      [rows][ld] dtype.
  *   ck        [rows][ldck] codes.   ck_exp [rows][ldexp], ceil(cols / 32) bytes.
  * A value is kept to 2^-4 of itself, or to 2^-17 of its block's largest where that is
- * more.  save's outputs may not overlap x, load's not ck or ck_exp.
+ * more.  save's outputs may not overlap x, load's not ck or ck_exp.  Every pointer is
+ * memory of the current device, and the stream is one of its.
  * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (negative size, ld < cols, ldexp < ceil(cols /
  * 32)), FP8_ERR_ARG (dtype), FP8_ERR_ALIGN (x, y: their element), FP8_ERR_UNSUPPORTED
  * (cols > 2^28).
