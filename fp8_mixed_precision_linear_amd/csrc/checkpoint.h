@@ -4,9 +4,10 @@
 // With a = max |x| of the block (an exact maximum) and e the largest integer with
 // a 2^e <= 448, |e| <= 126, a code is encode(x 2^e), x 2^e being exact, and the block's
 // byte is 127 - e: 2^(byte - 127) takes a code back to a value.  Nothing saturates; a
-// value is off by at most 2^-4 of itself, or 2^-10 2^-e, below 2^-17 of its block's
-// largest.  A block of zeros, or one that holds an infinity or a NaN, has e = 0, as in the
-// block casts.
+// value is off by at most 2^-4 of itself, or 2^-10 2^-e: below 2^-17 of its block's
+// largest, or, where e ends at 126, 2^-136 (a block that is below 2^-136 is lost).  What
+// rounds to 2^128 (from 1.9375 2^127 on) reads back as an infinity.  A block of zeros, or
+// one that holds an infinity or a NaN, has e = 0, as in the block casts.
 // 448 = 1.75 2^8, so with a = 1.m 2^(E - 127):  e = 8 - (E - 127) - (1.m > 1.75), and the
 // byte is E - 8 + (1.m > 1.75), at least 1 (a below 2^-118: e stays 126).
 #pragma once

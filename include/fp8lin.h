@@ -722,8 +722,11 @@ fp8_status fp8_gated_linear_plan(const fp8_gemm_args* gemm, const fp8_gated_args
  *   to its smallest normal value, in BF16); ck_exp is an E8M0 number (255: NaN).
  *   x, y      [rows][ld] dtype.
  *   ck        [rows][ldck] codes.   ck_exp [rows][ldexp], ceil(cols / 32) bytes.
- * A value is kept to 2^-4 of itself, or to 2^-17 of its block's largest where that is
- * more.  save's outputs may not overlap x, load's not ck or ck_exp.  Every pointer is
+ * A value of a block without infinities or NaN is kept to 2^-4 of itself, to 2^-17 of
+ * its block's largest or to 2^-136, whichever is most (the last only where the largest is
+ * below 2^-119: e ends at 126; all of a block below 2^-136 is lost).  From 1.9375 2^127
+ * on, a step from binary32's end, a value's code stands for 2^128, which load gives as an
+ * infinity.  save's outputs may not overlap x, load's not ck or ck_exp.  Every pointer is
  * memory of the current device, and the stream is one of its.
  * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (negative size, ld < cols, ldexp < ceil(cols /
  * 32)), FP8_ERR_ARG (dtype), FP8_ERR_ALIGN (x, y: their element), FP8_ERR_UNSUPPORTED
