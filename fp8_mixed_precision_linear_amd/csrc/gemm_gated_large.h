@@ -13,26 +13,35 @@ namespace fp8lin {
 
 namespace {
 
-// TI: 32 TI rows a tile (fewer than 256: no block scales).
-template <int AF, bool OUT8, typename Ep, typename StripEp, int TI = 8>
-hipError_t launch_gated_large_as(const GemmParams& p, const GatedParams& e, hipStream_t s) {
+// Per-tensor and per-row scales.  TI: 32 TI rows a tile (8 or 5).
+template <int AF, bool OUT8, typename Ep, int TI>
+hipError_t launch_gated_plain_as(const GemmParams& p, const GatedParams& e, hipStream_t s) {
   const int tm = (int)((p.M + 32 * TI - 1) / (32 * TI));
   const int tn = (int)(((Ep::PAIRED ? paired_columns(p.N) : p.N) + BN - 1) / BN);
   const dim3 grid((unsigned)(tm * tn)), block(W4_THREADS);
   const Ep ep{e};
-  if (p.a_scaling == 1 || p.a_scaling == 3) {
-    if constexpr (TI != 8) return hipErrorInvalidValue;   // (not planned)
-    else if (p.a_scaling == 1)
-      hipLaunchKernelGGL((k_gemm_big<AF, 0, true, true, false, false, OUT8, StripEp>), grid, dim3(THREADS), 0, s, p, tm,
-                         tn, StripEp{e});
-    else hipLaunchKernelGGL((k_gemm_w4<AF, 0, false, OUT8, W4_MX + 1, Ep>), grid, block, 0, s, p, tm, tn, ep);
-  } else if (p.a_scaling == 5 || p.b_scaling == 5) {
+  if (p.a_scaling == 5 || p.b_scaling == 5) {
     if (p.K % BK == 0) hipLaunchKernelGGL((k_gemm_w4<AF, 0, false, OUT8, W4_ROWS, Ep, TI>), grid, block, 0, s, p, tm, tn, ep);
     else hipLaunchKernelGGL((k_gemm_w4<AF, 0, true, OUT8, W4_ROWS, Ep, TI>), grid, block, 0, s, p, tm, tn, ep);
   } else {
     if (p.K % BK == 0) hipLaunchKernelGGL((k_gemm_w4<AF, 0, false, OUT8, W4_TENSOR, Ep, TI>), grid, block, 0, s, p, tm, tn, ep);
     else hipLaunchKernelGGL((k_gemm_w4<AF, 0, true, OUT8, W4_TENSOR, Ep, TI>), grid, block, 0, s, p, tm, tn, ep);
   }
+  return hipGetLastError();
+}
+
+// Every scaling, on 256 rows.
+template <int AF, bool OUT8, typename Ep, typename StripEp>
+hipError_t launch_gated_large_as(const GemmParams& p, const GatedParams& e, hipStream_t s) {
+  if (p.a_scaling != 1 && p.a_scaling != 3) return launch_gated_plain_as<AF, OUT8, Ep, 8>(p, e, s);
+  const int tm = (int)((p.M + BM - 1) / BM);
+  const int tn = (int)(((Ep::PAIRED ? paired_columns(p.N) : p.N) + BN - 1) / BN);
+  const dim3 grid((unsigned)(tm * tn));
+  if (p.a_scaling == 1)
+    hipLaunchKernelGGL((k_gemm_big<AF, 0, true, true, false, false, OUT8, StripEp>), grid, dim3(THREADS), 0, s, p, tm, tn,
+                       StripEp{e});
+  else
+    hipLaunchKernelGGL((k_gemm_w4<AF, 0, false, OUT8, W4_MX + 1, Ep>), grid, dim3(W4_THREADS), 0, s, p, tm, tn, Ep{e});
   return hipGetLastError();
 }
 

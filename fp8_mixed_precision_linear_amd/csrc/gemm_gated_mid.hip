@@ -11,8 +11,8 @@
 namespace fp8lin {
 
 hipError_t launch_gated_mid(const GemmParams& p, const GatedParams& e, hipStream_t s) {
-  return p.d_fp8 ? launch_gated_large_as<0, true, GatedStripEp, GatedStripEp, 5>(p, e, s)
-                 : launch_gated_large_as<0, false, GatedStripEp, GatedStripEp, 5>(p, e, s);
+  return p.d_fp8 ? launch_gated_plain_as<0, true, GatedStripEp, 5>(p, e, s)
+                 : launch_gated_plain_as<0, false, GatedStripEp, 5>(p, e, s);
 }
 
 }  // namespace fp8lin

@@ -80,9 +80,9 @@ struct TilePlace {
 // k_gemm_big; N a multiple of 128 in the block modes).  A DIRECT one takes the
 // accumulators as they are, rows and columns placed for it (TilePlace), and its first
 // reads are on their way before the last step.
-// TI: 16-row tiles of a wavefront, 8 unless the epilogue takes fewer (32 TI rows a
-// workgroup; the step's first TI / 2 row-tiles go row by row, the rest column by column;
-// 160 rows have three stages).
+// TI: 16-row tiles of a wavefront, 32 TI rows a workgroup: 8, or 5 for an epilogue that
+// goes by strips (160 rows, three stages; two row-tiles go row by row, three column by
+// column).
 template <int AF, int BF, bool KT, bool OUT8, int MODE, typename EP = NoEpilogue, int TI = 8>
 __global__ void __launch_bounds__(W4_THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
 k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
@@ -93,8 +93,8 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   static_assert(!(MX && KT), "block scales make K a multiple of the step");
   static_assert(!((PAIRED || DIRECT) && SB_COL), "pairs and placed tiles: blocks of B");
   constexpr int BMT = 32 * TI, R1 = TI / 2, R2 = TI - R1, NQ = TI + 8;   // rows, row-tiles of each part, DMA per stage
-  static_assert(TI == 8 || (TI >= 5 && TI < 8 && !DIRECT && !std::is_same_v<EP, NoEpilogue> && !MX),
-                "fewer rows: strips, no block scales");
+  static_assert(TI == 8 || (TI == 5 && !DIRECT && !std::is_same_v<EP, NoEpilogue> && !MX),
+                "160 rows: strips, no block scales");
   constexpr int AB = BMT * BK;   // B's place in a stage
   constexpr int NS = TI == 5 ? 3 : 2;   // stages: 160 rows leave room for a third
   // a stage: A, B, then (block modes) 256 row scales of A and of B
@@ -196,7 +196,7 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  // the first two stages go out together; wait for the first (NQ DMA
+  // the first NS stages go out together; wait for the first (NQ DMA
   // instructions per stage and wavefront, counted down in issue order)
 #pragma unroll
   for (int q = 0; q < NQ; ++q) load(0, lds[0], q);
@@ -276,17 +276,18 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   };
 
   // One K step on stage X, with B's fragments and row-tile 0's A fragment
-  // in registers; Y is the next step's stage.  The scheduling barriers keep
-  // the compiler to this order.
+  // in registers; Y is the next step's stage, and X is refilled with that of
+  // step kb + NS (of two stages: the step after next).  The scheduling
+  // barriers keep the compiler to this order.
   auto step = [&](auto dmatag, auto nexttag, auto lefttag, const uint8_t* X, const uint8_t* Y, int kb) {
-    constexpr bool DMA = decltype(dmatag)::value;    // issue the DMA of step kb + 2
+    constexpr bool DMA = decltype(dmatag)::value;    // issue the DMA of step kb + NS
     constexpr bool NEXT = decltype(nexttag)::value;  // read step kb + 1's fragments
-    constexpr int LEFT = decltype(lefttag)::value ? (NS - 2) * NQ : 0;   // DMA instructions of step kb + 2 in flight
+    constexpr int LEFT = decltype(lefttag)::value ? (NS - 2) * NQ : 0;   // (three stages) step kb + 2's DMA stays in flight
     uint32_t eu = 0;
     if constexpr (MX && !(SA_ROWS && SB_COL)) eu = __float_as_uint(su_tab[wave][kb]);
     __builtin_amdgcn_sched_barrier(0);
     // row-tiles 0..3 (R1 of them), row by row: the next row-tile's A fragment is read
-    // after this row's first MFMA, row-tile i + 4's after its fifth
+    // after this row's first MFMA, row-tile i + R1's after its fifth
 #pragma unroll
     for (int i = 0; i < R1; ++i) {
 #pragma unroll
@@ -312,8 +313,8 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
         for (int i = 0; i < R1; ++i) ea[i] = ea_of(Y, i);
       }
     }
-    // row-tiles 4..7, column by column: two DMA instructions of step kb + 2
-    // after the column's first and third MFMA, then B column-tile j, free
+    // row-tiles 4..7 (from R1 on), column by column: two DMA instructions of step
+    // kb + NS after the column's first and third MFMA, then B column-tile j, free
     // after its fourth, refilled from the next stage
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
