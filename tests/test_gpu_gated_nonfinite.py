@@ -17,7 +17,7 @@ INF = float("inf")
 # last columns are 32 of 256, their last rows 4 of 256
 PATHS = [
     (5, 203, 256, (5, 0), FEW, 16, False), (40, 203, 256, (5, 0), TILES, 32, False), (64, 520, 8192, (5, 0), TILES, 32, True),
-    (1037, 1999, 2320, (5, 5), TILES, 64, False), (2050, 4103, 656, (5, 0), TILES, 128, False),
+    (1037, 1999, 2320, (5, 5), TILES, 64, False), (1500, 4095, 656, (5, 0), TILES, 128, False),
     (2052, 4128, 640, (5, 0), LARGE, 256, False), (2052, 4128, 656, (5, 5), LARGE, 256, False),
     (2052, 4128, 640, (1, 2), LARGE, 256, False), (2052, 4128, 640, (3, 4), LARGE, 256, False)]
 
