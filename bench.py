@@ -779,8 +779,8 @@ def traffic_summarize(d, dst):
                 vals[int(r["Dispatch_Id"])][1] += float(r["Counter_Value"])
         return [vals[i] for i in sorted(vals)]
 
-    def nospace(t):   # (kernels without an epilogue carry its default type as their last argument)
-        return re.sub(r",[^,<>]*NoEpilogue", "", re.sub(r"\s", "", t))
+    def nospace(t):   # (kernels without an epilogue carry its default type, and k_gemm_w4 its 8 row-tiles, as last arguments)
+        return re.sub(r",[^,<>]*NoEpilogue(,8)?", "", re.sub(r"\s", "", t))
 
     def classify(rows):
         """(copy values, {class: [values]}): the launches in traffic_run's
