@@ -5,7 +5,11 @@
 // largest magnitude they exchange inside their quad; nothing is kept but the eight
 // values.  Bound: HBM (8192 x 8192 BF16 saved in 40.5 us, 5.0 TB/s, a copy's rate; 8192 x 14336
 // loaded in 63), small ones by a launch and a load's latency (1531 x 2053 FP32 7.4 us, of
-// which the call's host part is 5.5).  A row per workgroup and step: no lane has a division.
+// which the call's host part is 5.5).  A row per workgroup and step, 2048 columns of it: no
+// lane has a division, but lanes past a row's end have no work.  Widths that fill the
+// workgroups are at a copy's rate, others are not: 16.8 M values BF16 saved as 8192 x 2048 in 9.8
+// us, as 8192 x 2053 in 20.5, as 65536 x 256 in 41.5, as 262144 x 64 in 98 (loaded in 9.5, 14.1,
+// 30.8 and 35.8).
 #include "checkpoint.h"
 #include "launch.h"
 

@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(THREADS) k_gemm_big(GemmParams p, int tiles_m,
   const int64_t M = p.M, N = p.N, K = p.K;
   const int nk = (int)((K + BK - 1) / BK);
 
-  // ---- tile id: contiguous runs per XCD, grouped by 8 tile-rows
+  // ---- tile id: contiguous runs per XCD (of a multiple of 8 tiles; others as they
+  // come), grouped by 8 tile-rows
   const int nblk = tiles_m * tiles_n;
   int bid = blockIdx.x;
   if ((nblk & 7) == 0) bid = (bid & 7) * (nblk >> 3) + (bid >> 3);

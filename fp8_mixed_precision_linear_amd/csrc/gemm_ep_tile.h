@@ -69,7 +69,8 @@ __global__ void __launch_bounds__(EP_THREADS) __attribute__((amdgpu_waves_per_eu
   const int g = lane >> 4, l16 = lane & 15;
   const int64_t M = p.M, N = p.N, K = p.K;
 
-  // tile id as in the large kernels: contiguous runs per XCD, 8 tile-rows at a time
+  // tile id as in the large kernels: contiguous runs per XCD (of a multiple of 8 tiles), 8
+  // tile-rows at a time
   const int nblk = tiles_m * tiles_n;
   int bid = blockIdx.x;
   if ((nblk & 7) == 0) bid = (bid & 7) * (nblk >> 3) + (bid >> 3);

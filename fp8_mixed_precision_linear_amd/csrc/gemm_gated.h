@@ -675,7 +675,7 @@ struct GatedGradOp {
 };
 
 // The epilogue as k_gemm_big takes it (see LinearEp): two wavefronts on a SIMD hide what a
-// strip's way through LDS takes (8192 x 14336 x 4096 with 1x128 scales, backward: 570 us;
+// strip's way through LDS takes (8192 x 14336 x 4096 with 1x128 scales, backward, checkpoint: 570 us;
 // from the accumulators, as in gemm_gated_direct.h, 630).
 template <typename W, int TI, int TJ, int NW, typename Deq>
 __device__ __forceinline__ void gated_finish(const GemmParams& p, const GatedParams& e, const v4f (&acc)[TI][TJ], Deq&& deq,

@@ -13,7 +13,7 @@
 // With one wavefront on a SIMD nothing hides what an instruction takes: by way of LDS
 // (gemm_gated.h), 8192 x 28672 x 8192 took 1990 us backward (checkpoint, E5M2 codes, both
 // orders, bias gradient) and 2990 forward (checkpoint, E4M3 codes, both orders), here 1690
-// and 2710; fp8_scaled_gemm alone is 1400 and 2640.  Runs of 16 columns per lane that were
+// and 2760 (with the amax; 2745 the kernel); fp8_scaled_gemm alone is 1400 and 2640.  Runs of 16 columns per lane that were
 // not side by side cost 80 us more backward, and 16-byte halves of a row's 64 with BF16 400.
 // What is read beside the sums is on its way four rows ahead, the first rows before the last
 // step of K; every access is a buffer access whose range check drops rows and columns past

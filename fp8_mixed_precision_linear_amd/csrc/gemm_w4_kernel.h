@@ -113,7 +113,8 @@ k_gemm_w4(GemmParams p, int tiles_m, int tiles_n, EP ep) {
   const int64_t M = p.M, N = p.N, K = p.K;
   const int nk = (int)((K + BK - 1) / BK);
 
-  // ---- tile id: contiguous runs per XCD, grouped by 8 tile-rows
+  // ---- tile id: contiguous runs per XCD (of a multiple of 8 tiles; others as they
+  // come), grouped by 8 tile-rows
   const int nblk = tiles_m * tiles_n;
   int bid = blockIdx.x;
   if ((nblk & 7) == 0) bid = (bid & 7) * (nblk >> 3) + (bid >> 3);
